@@ -35,8 +35,12 @@ EXPORTS = ("ft_blob_stride", "ft_blob_layout", "ft_last_error", "ft_create", "ft
            "ft_kernel_timing_read", "ft_moe_layer_forward_noalloc", "ft_moe_stack_forward", "ft_last_routing",
            "ft_debug_device_wait", "ft_debug_host_wait_limit", "ft_debug_fail_copy", "ft_decode_geometry",
            "ft_debug_stack_epoch", "ft_flow_geometry", "ft_fp4_mma_probe", "ft_blob_layout_format",
-           "ft_cache_prefetch", "ft_debug_stack_timeline")
+           "ft_cache_prefetch", "ft_debug_stack_timeline", "ft_kv_workspace_bytes", "ft_kv_append", "ft_kv_attention",
+           "ft_kv_evict", "ft_kv_sync_status")
 FT_NOALLOC_SCRATCH_BYTES = 8 << 20
+FT_KV_BF16, FT_KV_E4M3 = 0, 1
+FT_KV_MASS = 1
+FT_ROPE_ADJACENT = 1
 KERNELS = ("router_logits", "topk", "permute", "gate_up", "down_combine", "quant_x", "gemm_gate_up", "gemm_down",
            "combine", "dec_stack", "quant_h")
 
@@ -64,6 +68,15 @@ class CacheStats(C.Structure):
                 ("overlap_ms", C.c_double), ("capacity_slots", C.c_int64),
                 ("used_slots", C.c_int64), ("mapped_bytes", C.c_int64), ("prefetches", C.c_int64),
                 ("prefetch_hits", C.c_int64), ("prefetch_bytes", C.c_int64)]
+
+
+class KvCache(C.Structure):
+    """ft_kv_cache: a layer's paged key-value cache (see make_kv)."""
+    _fields_ = [("head_dim", C.c_int32), ("n_heads", C.c_int32), ("n_kv_heads", C.c_int32), ("page_size", C.c_int32),
+                ("n_seqs", C.c_int32), ("max_pages", C.c_int32), ("n_pages", C.c_int64), ("format", C.c_int32),
+                ("k_scale", C.c_float), ("v_scale", C.c_float), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("mass", C.c_void_p), ("pos", C.c_void_p), ("block_table", C.c_void_p), ("lengths", C.c_void_p),
+                ("status", C.c_void_p)]
 
 
 _lib = None
@@ -118,6 +131,11 @@ def lib() -> C.CDLL:
         "ft_debug_stack_timeline": (ST, [P, P, I64]),
         "ft_fp4_mma_probe": (ST, [I64, P, P, C.POINTER(I32), P]),
         "ft_decode_geometry": (ST, [I32, I32, I32, C.POINTER(I64)]),
+        "ft_kv_workspace_bytes": (ST, [C.POINTER(KvCache), C.POINTER(I64)]),
+        "ft_kv_append": (ST, [C.POINTER(KvCache), I64, P, I64, P, I64, P, I64, P, P, I32, P, P, I32, P, U32, P]),
+        "ft_kv_attention": (ST, [C.POINTER(KvCache), P, I64, C.c_float, P, P, P, I64, U32, P]),
+        "ft_kv_evict": (ST, [C.POINTER(KvCache), P, I32, P, I64, P]),
+        "ft_kv_sync_status": (ST, [C.POINTER(KvCache), P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -377,3 +395,100 @@ def make_desc(hidden, inter, n_experts, top_k, n_layers=1, n_shared=0, cache_bud
               max_tokens=16, weight_format=0) -> ModelDesc:
     return ModelDesc(hidden, inter, n_experts, top_k, n_layers, n_shared, cache_budget_bytes, max_tokens,
                      weight_format)
+
+
+# ---------------------------------------------------------------------------
+# key-value cache
+# ---------------------------------------------------------------------------
+
+def make_kv(n_heads, k, v, block_table, lengths, mass=None, pos=None, k_scale=1.0, v_scale=1.0, status=None) -> KvCache:
+    """The ft_kv_cache of these tensors: k and v [n_pages][n_kv_heads][page_size][head_dim] in bf16 or
+    float8_e4m3fn, mass (fp32) and pos (int32) [n_pages][n_kv_heads][page_size] or None, block_table int32
+    [n_seqs][max_pages], lengths int32 [n_seqs], status int32 [1] or None.  It holds the tensors."""
+    if len(k.shape) != 4 or tuple(v.shape) != tuple(k.shape) or v.dtype != k.dtype:
+        raise ValueError(f"k {tuple(k.shape)} {k.dtype} and v {tuple(v.shape)} {v.dtype}: two pools "
+                         "[pages][KV heads][page size][head dim] of one type")
+    kind = str(k.dtype).rpartition(".")[2]
+    if kind not in ("bfloat16", "float8_e4m3fn"):
+        raise ValueError(f"pools of dtype {k.dtype}: bfloat16 or float8_e4m3fn")
+    for name, t, shape, dtype in (("mass", mass, k.shape[:3], "float32"), ("pos", pos, k.shape[:3], "int32"),
+                                  ("block_table", block_table, None, "int32"),
+                                  ("lengths", lengths, block_table.shape[:1], "int32"), ("status", status, (1,), "int32")):
+        if t is None and name in ("mass", "pos", "status"):
+            continue
+        if str(t.dtype).rpartition(".")[2] != dtype:
+            raise ValueError(f"{name} of dtype {t.dtype}: {dtype}")
+        if len(t.shape) != 2 if shape is None else tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} of shape {tuple(t.shape)}: "
+                             f"{'[n_seqs][max_pages]' if shape is None else tuple(shape)}")
+    n_pages, n_kv, page, d = k.shape
+    es = k.element_size()
+    kv = KvCache(d, n_heads, n_kv, page, block_table.shape[0], block_table.shape[1], n_pages,
+                 FT_KV_BF16 if kind == "bfloat16" else FT_KV_E4M3, k_scale, v_scale, _ptr(k, es), _ptr(v, es),
+                 _ptr(mass, 4), _ptr(pos, 4), _ptr(block_table, 4), _ptr(lengths, 4), _ptr(status, 4))
+    kv.tensors = (k, v, mass, pos, block_table, lengths, status)
+    return kv
+
+
+def _rows(t, name, heads, d) -> tuple[int, int]:
+    """Address and row stride (elements) of q, k or v [rows][heads][d]; rows may be apart, a row is dense."""
+    if tuple(t.shape[1:]) != (heads, d) or t.element_size() != 2:
+        raise ValueError(f"{name} {tuple(t.shape)} {t.dtype}: bf16 [rows][{heads}][{d}]")
+    s = t.stride()
+    if (s[2] != 1 and d > 1) or (s[1] != d and heads > 1):
+        raise ValueError(f"{name} of strides {s}: the heads of a row are dense")
+    return t.data_ptr(), s[0]
+
+
+def ft_kv_workspace_bytes(kv: KvCache) -> int:
+    n = I64()
+    _check(lib().ft_kv_workspace_bytes(C.byref(kv), C.byref(n)))
+    return n.value
+
+
+def ft_kv_append(kv: KvCache, q, k, v, cu_new, positions, inv_freq, axis, q_out, flags=0, stream=None) -> None:
+    """q [T][n_heads][D] and q_out (or None, both), k and v [T][n_kv_heads][D] (rows may be apart), cu_new int32
+    [n_seqs+1] or None, positions int32 [axes][T], inv_freq float64 and axis int32 [rot_dim/2] (or None, both: no
+    rotation)."""
+    d, hk = kv.head_dim, kv.n_kv_heads
+    kp, ks = _rows(k, "k", hk, d)
+    vp, vs = _rows(v, "v", hk, d)
+    qp, qs = _rows(q, "q", kv.n_heads, d) if q is not None else (None, 0)
+    T = k.shape[0]
+    if v.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError(f"q, k and v of different rows: {None if q is None else q.shape[0]}, {T}, {v.shape[0]}")
+    if q_out is not None and tuple(q_out.shape) != (T, kv.n_heads, d):
+        raise ValueError(f"q_out of shape {tuple(q_out.shape)}: {(T, kv.n_heads, d)}")
+    if cu_new is not None and tuple(cu_new.shape) != (kv.n_seqs + 1,):
+        raise ValueError(f"cu_new of shape {tuple(cu_new.shape)}: {(kv.n_seqs + 1,)}")
+    if positions is not None and (len(positions.shape) != 2 or positions.shape[1] != T):
+        raise ValueError(f"positions of shape {tuple(positions.shape)}: [axes][{T}]")
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    if (inv_freq is None) != (axis is None) or (axis is not None and tuple(axis.shape) != (half,)):
+        raise ValueError("inv_freq and axis: [rot_dim/2] each, or None")
+    _check(lib().ft_kv_append(C.byref(kv), T, qp, qs, kp, ks, vp, vs, _ptr(cu_new, 4), _ptr(positions, 4),
+                              0 if positions is None else positions.shape[0], _ptr(inv_freq, 8), _ptr(axis, 4),
+                              2 * half, _ptr(q_out, 2), flags, _stream(stream)))
+
+
+def ft_kv_attention(kv: KvCache, q, scale, out, lse, workspace, flags=0, stream=None) -> None:
+    """q [n_seqs][n_heads][D] (rows may be apart), out dense of that shape, lse float32 [n_seqs][n_heads] or None."""
+    qp, qs = _rows(q, "q", kv.n_heads, kv.head_dim)
+    if q.shape[0] != kv.n_seqs or tuple(out.shape) != tuple(q.shape):
+        raise ValueError(f"q {tuple(q.shape)} and out {tuple(out.shape)}: {kv.n_seqs} rows each")
+    if lse is not None and tuple(lse.shape) != (kv.n_seqs, kv.n_heads):
+        raise ValueError(f"lse of shape {tuple(lse.shape)}: {(kv.n_seqs, kv.n_heads)}")
+    _check(lib().ft_kv_attention(C.byref(kv), qp, qs, scale, _ptr(out, 2), _ptr(lse, 4), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), flags, _stream(stream)))
+
+
+def ft_kv_evict(kv: KvCache, budgets, recent, workspace, stream=None) -> None:
+    """budgets int32 [n_seqs]."""
+    if tuple(budgets.shape) != (kv.n_seqs,):
+        raise ValueError(f"budgets of shape {tuple(budgets.shape)}: {(kv.n_seqs,)}")
+    _check(lib().ft_kv_evict(C.byref(kv), _ptr(budgets, 4), recent, _ptr(workspace),
+                             workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def ft_kv_sync_status(kv: KvCache, stream=None) -> None:
+    _check(lib().ft_kv_sync_status(C.byref(kv), _stream(stream)))

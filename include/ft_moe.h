@@ -530,6 +530,139 @@ FT_API ft_status ft_moe_layer_forward_noalloc(int32_t hidden, int32_t inter, int
                                               const float* router_w, const float* logits_override, void* out,
                                               uint32_t flags, int32_t* status, void* stream);
 
+/* ---------------------------------------------------------------------- */
+/* key-value cache: the attention half of a decode step                    */
+/* ---------------------------------------------------------------------- */
+
+/* A layer's paged key-value cache, next to the expert cache above: an engine
+ * whose experts share the GPU with long contexts appends to it, attends over
+ * it and shrinks it by what it attends to.  Plain data that the caller fills
+ * and owns, with every buffer it names; the calls below keep nothing of it,
+ * allocate nothing, synchronise nothing (but ft_kv_sync_status) and may be
+ * captured into a CUDA graph.
+ *
+ * An entry is one token's key and value for one KV head, with the
+ * accumulated attention weight and the position that ft_kv_evict goes by.
+ * Sequence b's entries sit in slots 0 .. lengths[b]-1 of every KV head; slot i
+ * is entry i % page_size of page block_table[b][i / page_size].  Table entries
+ * past a sequence's last page are not read.  A row with length 0 is idle (a
+ * padded batch): no call reads or writes its pages.
+ *
+ * Pages: sequences may share a page that is only read (a common prefix).  A
+ * page that a call writes (ft_kv_append's new slots; every page, with
+ * FT_KV_MASS or ft_kv_evict) belongs to one sequence and stands once in the
+ * table; otherwise the order of the writes to it is open.
+ *
+ * Bad contents that only the device can see (a page outside [0, n_pages), a
+ * length that is negative or above max_pages * page_size, an axis or position
+ * out of range) set bit 2 of *status; the call skips the sequence (bad length)
+ * or the entry (bad page) and accesses nothing out of bounds. */
+typedef struct {
+  int32_t head_dim;      /* D: 64, 96, 128, 192 or 256 */
+  int32_t n_heads;       /* query heads, a multiple of n_kv_heads; the heads h*G .. h*G+G-1 share KV head h */
+  int32_t n_kv_heads;
+  int32_t page_size;     /* entries of a page: a power of two from 1 to 1024 */
+  int32_t n_seqs;        /* rows of block_table and lengths, at most 65536 (0: every call is a no-op) */
+  int32_t max_pages;     /* columns of block_table; max_pages * page_size <= 2^30 */
+  int64_t n_pages;       /* pages of the pools; n_pages * n_kv_heads * page_size < 2^31 */
+  int32_t format;        /* FT_KV_BF16 or FT_KV_E4M3 */
+  float k_scale;         /* what one unit of a stored key / value stands for (E4M3: positive and finite; */
+  float v_scale;         /*   BF16: 1) */
+  void* k;               /* dev [n_pages][n_kv_heads][page_size][D] */
+  void* v;               /* dev, the same */
+  float* mass;           /* dev fp32 [n_pages][n_kv_heads][page_size] accumulated attention weight, or NULL */
+  int32_t* pos;          /* dev int32, the same shape: the token's position on axis 0, or NULL */
+  const int32_t* block_table; /* dev int32 [n_seqs][max_pages] */
+  int32_t* lengths;      /* dev int32 [n_seqs] */
+  int32_t* status;       /* dev int32: device-detected errors are OR-ed into it (bit 2); NULL drops them */
+} ft_kv_cache;
+
+#define FT_KV_BF16 0
+#define FT_KV_E4M3 1        /* stored = E4M3(value / scale), nearest even, saturating at 448 */
+
+#define FT_KV_MASS 1u       /* ft_kv_attention: add every entry's weight to mass */
+#define FT_ROPE_ADJACENT 1u /* ft_kv_append: pairs (2i, 2i+1) instead of (i, i + rot_dim/2) */
+
+/* Bytes of the workspace that ft_kv_attention and ft_kv_evict take for this
+ * cache (one size covers both).  The workspace needs no initial contents and
+ * keeps none from one call for the next; calls that share one must be ordered
+ * on the GPU, so two graphs that may run at the same time take two.  Reads
+ * the shape only.  FT_ERR_INVALID on a bad shape. */
+FT_API ft_status ft_kv_workspace_bytes(const ft_kv_cache* kv, int64_t* bytes);
+
+/* Rotate the new tokens' queries and keys by their positions and write keys
+ * and values into the cache, before the step's attention.
+ *   T        new tokens.  The caller has already advanced lengths to count
+ *            them: sequence b's n_b new tokens go to its last n_b slots.
+ *   cu_new   dev int32 [n_seqs+1] or NULL: the tokens of sequence b are rows
+ *            cu_new[b] .. cu_new[b+1]-1 of q, k and v (cu_new[0] = 0,
+ *            ascending; rows from cu_new[n_seqs] on are padding and skipped).
+ *            NULL (decode): row b is sequence b's one new token, T = n_seqs,
+ *            idle rows are skipped.
+ *   q        dev bf16, row t at q + t*q_stride elements, [n_heads][D] dense
+ *            within a row; k and v the same with [n_kv_heads][D].  Strides are
+ *            multiples of 8 (q, k and v may be parts of one projection's
+ *            output).  q and q_out may both be NULL: keys and values only.
+ *   positions dev int32 [n_axes][T], not negative: one axis for text, three
+ *            (time, height, width) for images and video; n_axes 1 to 4.
+ *   inv_freq dev fp64 [rot_dim/2], axis dev int32 [rot_dim/2]: pair i turns
+ *            by positions[axis[i]][t] * inv_freq[i] radians, so that any
+ *            base, scaling and order of the axes' sections can be laid out
+ *            once by the caller.
+ *   rot_dim  0 or a multiple of 16 up to D: the leading elements that turn;
+ *            the others pass through.
+ *   q_out    dev bf16 [T][n_heads][D], dense; must not overlap q.  Rows of
+ *            skipped tokens are left as they were.
+ * Angles are taken in fp64, the rotation in fp32 with one rounding to bf16
+ * or E4M3.  New entries get mass 0 and their position (where those pools are
+ * not NULL).  Several tokens never share a slot, so the order of rows cannot
+ * matter.  Errors: FT_ERR_INVALID, FT_ERR_CUDA. */
+FT_API ft_status ft_kv_append(const ft_kv_cache* kv, int64_t T, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const int32_t* cu_new,
+                              const int32_t* positions, int32_t n_axes, const double* inv_freq, const int32_t* axis,
+                              int32_t rot_dim, void* q_out, uint32_t flags, void* stream);
+
+/* Attention of one new token a sequence over its cached entries:
+ *   p = softmax over the entries i of (scale * q . k_i), out = sum_i p_i v_i,
+ *   lse = log sum_i exp(scale * q . k_i).
+ *   q dev bf16, row b at q + b*q_stride elements (a multiple of 8), [n_heads][D]
+ *   dense within; out dev bf16 [n_seqs][n_heads][D], must not overlap q;
+ *   lse dev fp32 [n_seqs][n_heads] or NULL.  A row without entries gives
+ *   out = 0 and lse = -inf, and so does a head all of whose scores are -inf; a
+ *   NaN among a head's scores or a score of +inf gives NaN; a cached value
+ *   that is not finite gives an infinity or NaN in its own element of out.
+ *   With FT_KV_MASS, mass of entry i of KV head h += sum of p_i over the query
+ *   heads that share h (mass must not be NULL).
+ * Scores, softmax statistics and sums are fp32; out is rounded once to bf16.
+ * For a BF16 cache p meets v in two bf16 parts (16 bits of p); for an E4M3
+ * cache q is re-encoded as f16 with a power-of-two factor a head and p is
+ * rounded to f16 (11 bits), both exact next to what E4M3 rounded.  The work
+ * is split over the entries of all sequences by their lengths on the device
+ * and joined in a fixed order: the same inputs give the same bits on the same
+ * kind of GPU.  Errors: FT_ERR_INVALID, FT_ERR_CUDA. */
+FT_API ft_status ft_kv_attention(const ft_kv_cache* kv, const void* q, int64_t q_stride, float scale, void* out,
+                                 float* lse, void* workspace, int64_t workspace_bytes, uint32_t flags, void* stream);
+
+/* Shrink sequences to their budgets, by what was attended to.  For every
+ * sequence b with lengths[b] > budgets[b] (dev int32 [n_seqs], not negative)
+ * and every KV head by itself, budgets[b] entries survive:
+ *   first those with pos > newest pos of that head - recent (the newest
+ *   first), then those with the most mass; ties go to the lower slot.
+ * mass and pos must not be NULL; mass is not negative (a negative or NaN mass
+ * counts as 0), pos not negative.  Survivors in slots >= budgets[b] (ascending)
+ * move to the lowest evicted slots below it (key, value, mass and position),
+ * the rule of ft_expert_cache_resize; all others stay where they are.  Then
+ * lengths[b] = budgets[b], and the pages past it are the caller's to reuse.
+ * What slots at and above the new length hold is left as it was.
+ * recent >= 0.  Errors: FT_ERR_INVALID, FT_ERR_CUDA. */
+FT_API ft_status ft_kv_evict(const ft_kv_cache* kv, const int32_t* budgets, int32_t recent, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+
+/* Copy the cache's status word to the host (synchronising `stream`), clear
+ * it, and map it: bad contents -> FT_ERR_INVALID; else FT_OK (also without a
+ * status word). */
+FT_API ft_status ft_kv_sync_status(const ft_kv_cache* kv, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
