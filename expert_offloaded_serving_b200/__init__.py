@@ -78,6 +78,10 @@ class KvCache(C.Structure):
                 ("mass", C.c_void_p), ("pos", C.c_void_p), ("block_table", C.c_void_p), ("lengths", C.c_void_p),
                 ("status", C.c_void_p)]
 
+    @property
+    def ref(self):
+        return C.byref(self)
+
 
 _lib = None
 P = C.c_void_p
@@ -175,7 +179,7 @@ def _ptr(t, size: int | None = None) -> int | None:
 def _stream(s) -> int | None:
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -430,14 +434,23 @@ def make_kv(n_heads, k, v, block_table, lengths, mass=None, pos=None, k_scale=1.
     return kv
 
 
+def _dev(t, size: int) -> int | None:
+    """_ptr of a tensor (or None), by the short way where it is as it should be: these calls take microseconds."""
+    if t is None:
+        return None
+    if t.element_size() == size and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, size)
+
+
 def _rows(t, name, heads, d) -> tuple[int, int]:
     """Address and row stride (elements) of q, k or v [rows][heads][d]; rows may be apart, a row is dense."""
-    if tuple(t.shape[1:]) != (heads, d) or t.element_size() != 2:
-        raise ValueError(f"{name} {tuple(t.shape)} {t.dtype}: bf16 [rows][{heads}][{d}]")
-    s = t.stride()
-    if (s[2] != 1 and d > 1) or (s[1] != d and heads > 1):
-        raise ValueError(f"{name} of strides {s}: the heads of a row are dense")
-    return t.data_ptr(), s[0]
+    shape, (row, head, one) = t.shape, t.stride()
+    if shape[1] != heads or shape[2] != d or t.element_size() != 2:
+        raise ValueError(f"{name} {tuple(shape)} {t.dtype}: bf16 [rows][{heads}][{d}]")
+    if one != 1 or (head != d and heads > 1):
+        raise ValueError(f"{name} of strides {t.stride()}: the heads of a row are dense")
+    return t.data_ptr(), row
 
 
 def ft_kv_workspace_bytes(kv: KvCache) -> int:
@@ -450,45 +463,45 @@ def ft_kv_append(kv: KvCache, q, k, v, cu_new, positions, inv_freq, axis, q_out,
     """q [T][n_heads][D] and q_out (or None, both), k and v [T][n_kv_heads][D] (rows may be apart), cu_new int32
     [n_seqs+1] or None, positions int32 [axes][T], inv_freq float64 and axis int32 [rot_dim/2] (or None, both: no
     rotation)."""
-    d, hk = kv.head_dim, kv.n_kv_heads
+    d, hk, hq = kv.head_dim, kv.n_kv_heads, kv.n_heads
+    T = k.shape[0]
     kp, ks = _rows(k, "k", hk, d)
     vp, vs = _rows(v, "v", hk, d)
-    qp, qs = _rows(q, "q", kv.n_heads, d) if q is not None else (None, 0)
-    T = k.shape[0]
+    qp, qs = _rows(q, "q", hq, d) if q is not None else (None, 0)
     if v.shape[0] != T or (q is not None and q.shape[0] != T):
         raise ValueError(f"q, k and v of different rows: {None if q is None else q.shape[0]}, {T}, {v.shape[0]}")
-    if q_out is not None and tuple(q_out.shape) != (T, kv.n_heads, d):
-        raise ValueError(f"q_out of shape {tuple(q_out.shape)}: {(T, kv.n_heads, d)}")
-    if cu_new is not None and tuple(cu_new.shape) != (kv.n_seqs + 1,):
+    if q_out is not None and q_out.shape != (T, hq, d):
+        raise ValueError(f"q_out of shape {tuple(q_out.shape)}: {(T, hq, d)}")
+    if cu_new is not None and cu_new.shape != (kv.n_seqs + 1,):
         raise ValueError(f"cu_new of shape {tuple(cu_new.shape)}: {(kv.n_seqs + 1,)}")
-    if positions is not None and (len(positions.shape) != 2 or positions.shape[1] != T):
+    if positions is not None and (positions.dim() != 2 or positions.shape[1] != T):
         raise ValueError(f"positions of shape {tuple(positions.shape)}: [axes][{T}]")
     half = 0 if inv_freq is None else inv_freq.shape[0]
-    if (inv_freq is None) != (axis is None) or (axis is not None and tuple(axis.shape) != (half,)):
+    if (inv_freq is None) != (axis is None) or (axis is not None and axis.shape != (half,)):
         raise ValueError("inv_freq and axis: [rot_dim/2] each, or None")
-    _check(lib().ft_kv_append(C.byref(kv), T, qp, qs, kp, ks, vp, vs, _ptr(cu_new, 4), _ptr(positions, 4),
-                              0 if positions is None else positions.shape[0], _ptr(inv_freq, 8), _ptr(axis, 4),
-                              2 * half, _ptr(q_out, 2), flags, _stream(stream)))
+    _check(lib().ft_kv_append(kv.ref, T, qp, qs, kp, ks, vp, vs, _dev(cu_new, 4), _dev(positions, 4),
+                              0 if positions is None else positions.shape[0], _dev(inv_freq, 8), _dev(axis, 4),
+                              2 * half, _dev(q_out, 2), flags, _stream(stream)))
 
 
 def ft_kv_attention(kv: KvCache, q, scale, out, lse, workspace, flags=0, stream=None) -> None:
-    """q [n_seqs][n_heads][D] (rows may be apart), out dense of that shape, lse float32 [n_seqs][n_heads] or None."""
+    """q [n_seqs][n_heads][D] (rows may be apart), out dense of that shape, lse float32 [n_seqs][n_heads] or None,
+    workspace uint8."""
     qp, qs = _rows(q, "q", kv.n_heads, kv.head_dim)
-    if q.shape[0] != kv.n_seqs or tuple(out.shape) != tuple(q.shape):
+    if q.shape[0] != kv.n_seqs or out.shape != q.shape:
         raise ValueError(f"q {tuple(q.shape)} and out {tuple(out.shape)}: {kv.n_seqs} rows each")
-    if lse is not None and tuple(lse.shape) != (kv.n_seqs, kv.n_heads):
+    if lse is not None and lse.shape != (kv.n_seqs, kv.n_heads):
         raise ValueError(f"lse of shape {tuple(lse.shape)}: {(kv.n_seqs, kv.n_heads)}")
-    _check(lib().ft_kv_attention(C.byref(kv), qp, qs, scale, _ptr(out, 2), _ptr(lse, 4), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), flags, _stream(stream)))
+    _check(lib().ft_kv_attention(kv.ref, qp, qs, scale, _dev(out, 2), _dev(lse, 4), _dev(workspace, 1),
+                                 workspace.numel(), flags, _stream(stream)))
 
 
 def ft_kv_evict(kv: KvCache, budgets, recent, workspace, stream=None) -> None:
-    """budgets int32 [n_seqs]."""
-    if tuple(budgets.shape) != (kv.n_seqs,):
+    """budgets int32 [n_seqs], workspace uint8."""
+    if budgets.shape != (kv.n_seqs,):
         raise ValueError(f"budgets of shape {tuple(budgets.shape)}: {(kv.n_seqs,)}")
-    _check(lib().ft_kv_evict(C.byref(kv), _ptr(budgets, 4), recent, _ptr(workspace),
-                             workspace.numel() * workspace.element_size(), _stream(stream)))
+    _check(lib().ft_kv_evict(kv.ref, _dev(budgets, 4), recent, _dev(workspace, 1), workspace.numel(), _stream(stream)))
 
 
 def ft_kv_sync_status(kv: KvCache, stream=None) -> None:
-    _check(lib().ft_kv_sync_status(C.byref(kv), _stream(stream)))
+    _check(lib().ft_kv_sync_status(kv.ref, _stream(stream)))

@@ -40,8 +40,8 @@ ft_status check_shape(const ft_kv_cache* c) {
   if (c->n_kv_heads <= 0 || c->n_heads <= 0 || c->n_heads % c->n_kv_heads || c->n_heads > 65536)
     return refuse(FT_ERR_INVALID, "n_heads %d is not a positive multiple of n_kv_heads %d, at most 65536", c->n_heads,
                   c->n_kv_heads);
-  if (c->page_size < 1 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
-    return refuse(FT_ERR_INVALID, "page_size %d is not a power of two from 1 to 1024", c->page_size);
+  if (c->page_size < 8 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+    return refuse(FT_ERR_INVALID, "page_size %d is not a power of two from 8 to 1024", c->page_size);
   if (c->n_seqs < 0 || c->n_seqs > ft::kKvMaxSeqs)
     return refuse(FT_ERR_INVALID, "n_seqs %d not in [0, %d]", c->n_seqs, ft::kKvMaxSeqs);
   if (c->max_pages < 1 || (int64_t)c->max_pages * c->page_size > (1 << 30))
@@ -267,6 +267,7 @@ extern "C" ft_status ft_kv_sync_status(const ft_kv_cache* kv, void* stream) {
     KV_TRY(cu("status", cudaMemsetAsync(kv->status, 0, sizeof bits, s)));
   }
   KV_TRY(cu("synchronise", cudaStreamSynchronize(s)));
+  if (bits & ft::kStTimeout) return refuse(FT_ERR_TIMEOUT, "a wait for a copy inside the GPU gave up");
   if (bits & ft::kStBadId)
     return refuse(FT_ERR_INVALID, "the cache's contents: a page, length, position, axis or budget out of range");
   return FT_OK;

@@ -29,75 +29,111 @@
 // With FT_KV_MASS the scores go to the workspace as they come (G fp32 values
 // an entry, next to 4 D bytes of it), and k_kv_mass turns them into weights
 // once the row's lse is known.
+#include "ft_gemm.h"
 #include "ft_kv.cuh"
+#include "ft_tc.cuh"
 
 namespace ft {
 
 namespace {
 
-constexpr int kTile = 16;        // entries of a tile
 constexpr int kRows = 16;        // query heads of an item: rows of the mma tile
-constexpr int kMaxWarps = 8;     // warps of a block at most
+constexpr int kMaxWarps = 16;     // warps of a block at most
 constexpr int kMaxChunks = kKvMaxSms * kMaxWarps;
-constexpr int kRingBytes = 212 * 1024;  // shared memory of a block's rings at most
 
-// The ring of a warp for entries of RB bytes a side: a stage holds 16 keys and 16
-// values, rows 16 bytes apart from a multiple of 128 (ldmatrix then reads 8 rows
-// from 8 different groups of banks), and the 16 row numbers.
+// The ring of a warp for entries of RB bytes a side: a stage holds a tile of keys
+// and one of values as TMA leaves them, boxes of kBox bytes x the tile's rows whose
+// 16-byte pieces are swizzled (ldmatrix then reads 8 rows from 8 different
+// groups of banks).
+#ifndef TUNE_TILE
+#define TUNE_TILE(RB) (RB <= 256 ? 32 : 16)
+#define TUNE_WARPS(RB) (RB == 256 ? 6 : RB >= 384 ? 4 : 8)
+#define TUNE_MIN 32
+#endif
 template <int RB>
 struct Ring {
-  static constexpr int kStride = RB + 16;
-  static constexpr int kSide = kTile * kStride;
-  static constexpr int kStage = 2 * kSide + kTile * 4;
-  static constexpr int kWarps = 2 * kSide > 12000 ? 4 : 8;
-  static constexpr int kFit = kRingBytes / (kWarps * kStage);
+  static constexpr int kTile = TUNE_TILE(RB);  // entries
+  static constexpr int kBox = RB % 128 == 0 ? 128 : RB % 64 == 0 ? 64 : 32;
+  static constexpr int kBoxes = RB / kBox;
+  static constexpr int kBoxBytes = kTile * kBox;
+  static constexpr int kSide = kTile * RB;
+  static constexpr int kStage = 2 * kSide;
+  static constexpr int kWarps = TUNE_WARPS(RB);
+  static constexpr int kFit = 220 * 1024 / (kWarps * kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  static constexpr int kBytes = kWarps * kStages * kStage;
+  static constexpr int kBytes = kWarps * kStages * kStage + 1024;  // the swizzle goes by address: aligned to its period
 };
 
-// What k_kv_split leaves for the kernels behind it.
-struct Going {  // the row that goes on past the end of a chunk
-  int b, hh;      // sequence (-1: none) and item of it
-  int j0, parts;  // the chunk it begins on, the chunks it lies on
+constexpr int tile_of(int row_bytes) { return TUNE_TILE(row_bytes); }
+
+// What chunk j leaves for block j of k_kv_join.
+struct __align__(16) Chunk {
+  int b, hh, first, len;  // sequence and item of its first tile, that row's first tile in the batch and its entries
+  int tiles, size;        // its tiles (0: none), tiles of a chunk in this launch
+  int go_b, go_hh;        // the row that goes on past its end (go_b -1: none)
+  int go_j0, go_parts;    // the chunk that row begins on, the chunks it lies on
+  int pad[2];
 };
 struct AttnWork {
-  Going* going;      // [chunks]
-  int4* start;       // [chunks] where the chunk begins: sequence (-1: empty chunk), item, tile of the item, tiles of the chunk
-  float2* ml;        // [chunks][2][16] m and l of a part (log2 units); part 0: a row that came in, 1: one that goes on
+  Chunk* chunks;
+  float2* ml;        // [chunks][2][16] m and l of a part (log2 units); side 0: a row that came in, 1: one that goes on
   float* o;          // [chunks][2][16][D]
-  float* lse2;       // [n_seqs][Hq] lse in log2 units (mass)
-  float* scores;     // [rows / page][G][page] scores in log2 units (mass)
+  float* lse2;       // [n_seqs][Hq] lse of whole rows in log2 units (mass)
+  float* scores;     // [tiles][8 or 16 rows][entries of a tile] scores in log2 units (mass)
+  int64_t tiles;     // that `scores` holds
 };
 
 __host__ __device__ inline int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
-__host__ __device__ inline int64_t carve(AttnWork& w, uint8_t* base, int D, int n_seqs, int Hq, int64_t rows, int G) {
+// Scores of the tiles that sequences of their own pages can have: every row of the pool, and a last tile each.
+inline int64_t carve(AttnWork& w, uint8_t* base, int D, int row_bytes, int n_seqs, int Hq, int Hkv, int64_t rows, bool mass) {
+  const int G = Hq / Hkv, tile = tile_of(row_bytes);
   int64_t at = 0;
-  w.going = reinterpret_cast<Going*>(base + at);
-  at += up256((int64_t)kMaxChunks * sizeof(Going));
-  w.start = reinterpret_cast<int4*>(base + at);
-  at += up256((int64_t)kMaxChunks * sizeof(int4));
+  w.chunks = reinterpret_cast<Chunk*>(base + at);
+  at += up256((int64_t)kMaxChunks * sizeof(Chunk));
   w.ml = reinterpret_cast<float2*>(base + at);
   at += up256((int64_t)kMaxChunks * 2 * kRows * sizeof(float2));
   w.o = reinterpret_cast<float*>(base + at);
   at += up256((int64_t)kMaxChunks * 2 * kRows * D * sizeof(float));
   w.lse2 = reinterpret_cast<float*>(base + at);
+  w.scores = nullptr;
+  w.tiles = 0;
+  if (!mass) return at;
   at += up256((int64_t)n_seqs * Hq * sizeof(float));
   w.scores = reinterpret_cast<float*>(base + at);
-  at += up256(rows * G * (int64_t)sizeof(float));
+  w.tiles = (rows / tile + (int64_t)n_seqs * Hkv) * ((G + kRows - 1) / kRows);
+  at += up256(w.tiles * tile * (G > 8 ? 16 : 8) * (int64_t)sizeof(float));
   return at;
 }
 
 struct SplitArgs {
+  CUtensorMap k_map, v_map;  // rows of the pools, boxes of kBox bytes x box_rows
   KvAttnArgs a;
   AttnWork w;
-  int groups;  // items of a KV head: groups of 16 query heads
+  int groups;     // items of a KV head: groups of 16 query heads
+  int box_shift;  // box_rows = 1 << box_shift: a tile's rows, or a page's where pages are smaller
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+// Wait for phase `parity`; false after tc::kWaitNs.  The timer is read once the wait has
+// already taken many polls.
+__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity) {
+  const uint32_t at = smem_u32(bar);
+  uint64_t since = 0;
+  for (uint32_t n = 1;; n++) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(at), "r"(parity)
+                 : "memory");
+    if (ok) return true;
+    if ((n & 255) == 0) {
+      const uint64_t now = tc::gtime();
+      if (since == 0) since = now;
+      else if (now - since > tc::kWaitNs) return false;
+    }
+  }
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
@@ -115,22 +151,29 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
 
 // c += A(16 x 16) B(16 x 8), fp32 accumulators.
 template <bool F16>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   if (F16)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
   else
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// Two E4M3 bytes (low half of v) as f16x2, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
-  uint32_t h;
-  asm("{ .reg .b16 b; cvt.u16.u32 b, %1; cvt.rn.f16x2.e4m3x2 %0, b; }" : "=r"(h) : "r"(v));
-  return h;
+// 8 x 8 values of 16 bits, transposed over the warp.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Four E4M3 bytes as two f16x2 (bytes 0, 1 and bytes 2, 3), exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -155,52 +198,73 @@ struct Place {
   int b, hh, t, len, nt;
 };
 
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+template <int TILE>
+__device__ __forceinline__ int tiles_of(int len) {
+  return (len + TILE - 1) / TILE;
+}
 
+template <int TILE>
 __device__ __forceinline__ void next_sequence(const KvView& kv, Place& p) {
   do {
     p.b++;
     p.len = p.b < kv.n_seqs ? kv_length(kv, p.b) : 1;
   } while (p.len == 0);
-  p.nt = tiles_of(p.len);
+  p.nt = tiles_of<TILE>(p.len);
 }
 
+template <int TILE>
 __device__ __forceinline__ void advance(const KvView& kv, Place& p, int items) {
   if (++p.t < p.nt) return;
   p.t = 0;
   if (++p.hh < items) return;
   p.hh = 0;
-  next_sequence(kv, p);
+  next_sequence<TILE>(kv, p);
 }
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
-// D: head_dim.  E4M3: the cache's format.  WIDE: more than 8 query heads in an
-// item (else rows 8 to 15 of the tile are idle and their registers are not kept).
-// MASS: scores go to the workspace.
-template <int D, bool E4M3, bool WIDE, bool MASS>
-__global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv_split(SplitArgs args) {
+// Tiles a warp takes at least: a row of few entries is read by few warps, whose
+// parts need no (or a short) join.
+constexpr int kMinEntries = TUNE_MIN;
+
+// A running maximum is replaced once a score passes it by this much (a factor of
+// 256): any reference would do for the sums, and most tiles then need neither
+// the maximum over the warp's lanes nor the rescaling of O.  p stays below 2^8,
+// within f16.
+constexpr float kSlack = 8.0f;
+
+// D: head_dim.  E4M3: the cache's format.  NB: blocks of 8 query heads of an
+// item.  MASS: scores go to the workspace.
+template <int D, bool E4M3, int NB, bool MASS>
+__global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv_split(const __grid_constant__ SplitArgs args) {
   constexpr int RB = D * (E4M3 ? 1 : 2);
   using R = Ring<RB>;
+  constexpr int TILE = R::kTile, NT = TILE / 16;       // entries of a tile, steps of 16
   constexpr int kThreads = R::kWarps * 32;
-  constexpr int kChunksRow = RB / 16;                  // 16-byte pieces of a row
-  constexpr int kCopies = kTile * kChunksRow / 32;     // cp.async a lane and side
-  constexpr int NR = WIDE ? 2 : 1;                     // rows of the tile a lane keeps
+  constexpr int kPieces = RB / 16, kBoxPieces = R::kBox / 16;  // 16-byte pieces of a row, of its part in a box
+  constexpr int KC = NT * NB >= 4 ? 1 : 4 / (NT * NB);
+  constexpr uint32_t kFull = TILE == 32 ? 0xffffffffu : 0xffffu;
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t s_full[R::kWarps * R::kStages];
+  __shared__ uint32_t s_there[R::kWarps * R::kStages];  // entries of a stage's tile that exist, a bit each
   __shared__ int s_sum[kThreads + 1];
+  __shared__ int s_warp[R::kWarps];
 
   const KvView& kv = args.a.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = kv.Hkv * args.groups;
 
   kv_pdl_trigger();
+  uint64_t* const full = s_full + warp * R::kStages;
+  if (lane < R::kStages) tc::mbar_init(full + lane, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   // Tiles of the batch and where each thread's share of the sequences begins.
   const int per = (kv.n_seqs + kThreads - 1) / kThreads;
   {
     int sum = 0;
     for (int i = 0; i < per; i++) {
       const int b = tid * per + i;
-      if (b < kv.n_seqs) sum += tiles_of(kv_length(kv, b, blockIdx.x == 0)) * items;
+      if (b < kv.n_seqs) sum += tiles_of<TILE>(kv_length(kv, b, blockIdx.x == 0)) * items;
     }
     int run = sum;
 #pragma unroll
@@ -208,7 +272,6 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
       const int x = __shfl_up_sync(0xffffffffu, run, d);
       if (lane >= d) run += x;
     }
-    __shared__ int s_warp[R::kWarps];
     if (lane == 31) s_warp[warp] = run;
     __syncthreads();
     for (int w = 0; w < warp; w++) run += s_warp[w];
@@ -225,21 +288,18 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
       for (int i = tid; i < kv.Hq; i += kThreads) args.a.lse[(int64_t)b * kv.Hq + i] = kNegInf;
   }
 
-  const int total = s_sum[kThreads];
-  const int chunk = max(1, (total + (int)gridDim.x * R::kWarps - 1) / ((int)gridDim.x * R::kWarps));
+  const int total = s_sum[kThreads], warps = (int)gridDim.x * R::kWarps;
+  const int chunk = max(kMinEntries / TILE, (total + warps - 1) / warps);
   const int j = warp * gridDim.x + blockIdx.x;  // neighbours in the batch sit on different SMs
   const int lo = (int)min((int64_t)j * chunk, (int64_t)total), hi = min(lo + chunk, total);
   if (lo >= hi) {
-    if (lane == 0) {
-      args.w.going[j] = Going{-1, 0, 0, 0};
-      if (MASS) args.w.start[j] = make_int4(-1, 0, 0, 0);
-    }
+    if (lane == 0) args.w.chunks[j] = Chunk{-1, 0, 0, 0, 0, chunk, -1, 0, 0, 0, {0, 0}};
     return;
   }
 
   // The place of tile `lo`: the thread share that holds it, then its sequences.
   Place cons;
-  int base;  // first tile of sequence cons.b
+  int row_first;  // first tile of the present row in the batch's order
   {
     int l = 0, h = kThreads;  // s_sum[l] <= lo < s_sum[h]
     while (h - l > 1) {
@@ -247,60 +307,70 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
       if (s_sum[m] <= lo) l = m;
       else h = m;
     }
-    base = s_sum[l];
+    int base = s_sum[l];
     cons.b = l * per;
     for (;; cons.b++) {
       cons.len = kv_length(kv, cons.b);
-      cons.nt = tiles_of(cons.len);
+      cons.nt = tiles_of<TILE>(cons.len);
       if (lo < base + cons.nt * items) break;
       base += cons.nt * items;
     }
     cons.hh = (lo - base) / cons.nt;
     cons.t = (lo - base) - cons.hh * cons.nt;
+    row_first = lo - cons.t;
   }
-  if (MASS && lane == 0) args.w.start[j] = make_int4(cons.b, cons.hh, cons.t, hi - lo);
+  Chunk left{cons.b, cons.hh, row_first, cons.len, hi - lo, chunk, -1, 0, 0, 0, {0, 0}};
 
-  uint8_t* const ring = smem + warp * (R::kStages * R::kStage);
+  uint8_t* const ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u) + warp * (R::kStages * R::kStage);
   const uint32_t ring32 = smem_u32(ring);
+  uint32_t* const there_of = s_there + warp * R::kStages;
 
-  // ---- producer: rows of a tile, then their copies ----
+  // ---- producer: the tile's rows, a box (of one page) for each of the first lanes ----
   Place prod = cons;
-  auto tile_row = [&](const Place& p) {  // lanes 0..15: row of entry lane of the tile, -1 past the end
-    const int slot = p.t * kTile + (lane & 15);
-    return slot < p.len && p.b < kv.n_seqs ? kv_row(kv, p.b, p.hh / args.groups, slot) : -1;
+  const int box_shift = args.box_shift, box_bytes = RB << box_shift;
+  auto box_row = [&](const Place& p) {  // first row of the lane's box, -1 where there is none
+    const int slot = p.t * TILE + (lane << box_shift);
+    return lane < (TILE >> box_shift) && slot < p.len && p.b < kv.n_seqs ? kv_row(kv, p.b, p.hh / args.groups, slot) : -1;
   };
-  int row_next = tile_row(prod);
+  int row_next = box_row(prod), left_next = prod.len - prod.t * TILE;
   int to_load = hi - lo;
   auto load = [&](int stage) {
+    if (to_load <= 0) return;
+    to_load--;
+    const int row = row_next, left = left_next;
     if (to_load > 0) {
-      to_load--;
-      const int row = row_next;
-      if (to_load > 0) {
-        advance(kv, prod, items);
-        row_next = tile_row(prod);
-      }
-      const uint32_t k_at = ring32 + stage * R::kStage, v_at = k_at + R::kSide;
-      if (lane < kTile) *reinterpret_cast<int*>(ring + stage * R::kStage + 2 * R::kSide + lane * 4) = row;
+      advance<TILE>(kv, prod, items);
+      row_next = box_row(prod);
+      left_next = prod.len - prod.t * TILE;
+    }
+    const uint32_t boxes = __ballot_sync(0xffffffffu, row >= 0);
+    const uint32_t there = __ballot_sync(0xffffffffu, lane < TILE && lane < left && ((boxes >> (lane >> box_shift)) & 1u));
+    if (lane == 0) {
+      there_of[stage] = there;
+      tc::mbar_expect(full + stage, (uint32_t)(__popc(boxes) * box_bytes * 2));
+    }
+    __syncwarp();
+    if (row >= 0) {
+      uint8_t* const at = ring + stage * R::kStage + ((lane << box_shift) * R::kBox);
 #pragma unroll
-      for (int i = 0; i < kCopies; i++) {
-        const int c = i * 32 + lane, r = c / kChunksRow, col = c - r * kChunksRow;
-        const int from = __shfl_sync(0xffffffffu, row, r);
-        const bool real = from >= 0;
-        const int64_t off = (int64_t)(real ? from : 0) * RB + col * 16;
-        cp16(k_at + r * R::kStride + col * 16, kv.k + off, real);
-        cp16(v_at + r * R::kStride + col * 16, kv.v + off, real);
+      for (int i = 0; i < R::kBoxes; i++) {
+        tc::tma_2d(at + i * R::kBoxBytes, &args.k_map, i * R::kBox, row, full + stage);
+        tc::tma_2d(at + R::kSide + i * R::kBoxBytes, &args.v_map, i * R::kBox, row, full + stage);
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < R::kStages - 1; s++) load(s);
 
   // ---- consumer ----
-  const int g = lane >> 2, j2 = (lane & 3) * 2;  // the mma layout's row and first column
-  uint32_t qf[D / 16][4];
-  float o[D / 8][4];
-  float m[NR], l[NR], qs[NR];
+  // S^T = K Q^T: 16 entries x 8 heads, O^T = V^T P^T: 16 dims x 8 heads.  A lane
+  // (g, j) of the mma layout has the heads 2j and 2j+1 of each block, the entries g
+  // and g + 8 of S^T; P^T becomes the second product's operand by two transposes of
+  // 8 x 8.
+  const int g = lane >> 2, j2 = (lane & 3) * 2;
+  uint32_t q[D / 16][NB][2];
+  float o[D / 16][NB][4];
+  float m[NB][2], l[NB][2], qs[NB][2];
   int n_rows = 0, head0 = 0;
 
   auto begin_row = [&](int b, int hh) {
@@ -309,22 +379,20 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     n_rows = min(kRows, kv.G - gi * kRows);
     const float unit = args.a.scale * 1.4426950408889634f * kv.k_scale;
 #pragma unroll
-    for (int r = 0; r < 2; r++) {
-      if (r >= NR) {
+    for (int nb = 0; nb < NB; nb++) {
+      const bool real = g + 8 * nb < n_rows;
+      const uint16_t* src = args.a.q + (int64_t)b * args.a.q_stride + (int64_t)(head0 + (real ? g + 8 * nb : 0)) * D;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks++) qf[ks][1] = qf[ks][3] = 0u;
-        continue;
+      for (int i = 0; i < 2; i++) {
+        m[nb][i] = kNegInf;
+        l[nb][i] = 0.0f;
+        qs[nb][i] = unit;
       }
-      const bool real = g + 8 * r < n_rows;
-      const uint16_t* q = args.a.q + (int64_t)b * args.a.q_stride + (int64_t)(head0 + (real ? g + 8 * r : 0)) * D;
-      m[r] = kNegInf;
-      l[r] = 0.0f;
-      qs[r] = unit;
       if (!E4M3) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ks++) {
-          qf[ks][r] = real ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + j2) : 0u;
-          qf[ks][2 + r] = real ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + j2) : 0u;
+          q[ks][nb][0] = real ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + j2) : 0u;
+          q[ks][nb][1] = real ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + j2) : 0u;
         }
       } else {
         // The 16 contraction steps of an mma take the dims 4i, 4i+1 (first half)
@@ -332,371 +400,497 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
         // ldmatrix hands out the bytes of a key.  q joins them as f16 with a
         // power-of-two factor that puts the head's largest magnitude into
         // [2^14, 2^15): exact for bf16 values down to 2^-28 of it.
-        uint2 raw[D / 16];
         float top = 0.0f;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ks++) {
-          raw[ks] = real ? *reinterpret_cast<const uint2*>(q + ks * 16 + 2 * j2) : make_uint2(0u, 0u);
-          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(raw[ks].x)), fabsf(bf16_hi(raw[ks].x))),
-                                 fmaxf(fabsf(bf16_lo(raw[ks].y)), fabsf(bf16_hi(raw[ks].y)))));
+          const uint2 raw = real ? *reinterpret_cast<const uint2*>(src + ks * 16 + 2 * j2) : make_uint2(0u, 0u);
+          q[ks][nb][0] = raw.x;
+          q[ks][nb][1] = raw.y;
+          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(raw.x)), fabsf(bf16_hi(raw.x))),
+                                 fmaxf(fabsf(bf16_lo(raw.y)), fabsf(bf16_hi(raw.y)))));
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent; 0 and 255: as it is
         const bool usual = e > 14 && e < 255;
         const float up = usual ? __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23) : 1.0f;
-        qs[r] = usual ? unit * __uint_as_float((uint32_t)(e - 14) << 23) : unit;
+        const float down = usual ? unit * __uint_as_float((uint32_t)(e - 14) << 23) : unit;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks++) {
-          qf[ks][r] = f16x2(bf16_lo(raw[ks].x) * up, bf16_hi(raw[ks].x) * up);
-          qf[ks][2 + r] = f16x2(bf16_lo(raw[ks].y) * up, bf16_hi(raw[ks].y) * up);
-        }
+        for (int i = 0; i < 2; i++) qs[nb][i] = __shfl_sync(0xffffffffu, down, (j2 + i) * 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ks++)
+#pragma unroll
+          for (int i = 0; i < 2; i++)
+            q[ks][nb][i] = f16x2(bf16_lo(q[ks][nb][i]) * up, bf16_hi(q[ks][nb][i]) * up);
       }
     }
 #pragma unroll
-    for (int n = 0; n < D / 8; n++)
+    for (int n = 0; n < D / 16; n++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) o[n][i] = 0.0f;
+      for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) o[n][nb][i] = 0.0f;
   };
 
-  // Element (row r of the lane, n-tile, side) of O sits at these dims: BF16
-  // n-tile n covers dims 8n .. 8n+7; E4M3 n-tiles 2c and 2c+1 cover the even
-  // and odd dims of the 16 from 16c on.
-  auto end_row = [&](int b, bool whole, int part) {
+  // Rows g and g + 8 of the n-th block of O^T are the dims 16n + g and 16n + g + 8
+  // (BF16), 16n + 2g and 16n + 2g + 1 (E4M3).
+  auto end_row = [&](int b, bool whole, int side) {
 #pragma unroll
-    for (int r = 0; r < NR; r++) {
-      float sum = l[r];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int row = g + 8 * r;
-      if (row >= n_rows) continue;
-      if (whole) {
-        const float inv = sum == 0.0f ? 0.0f : kv.v_scale / sum;
-        uint16_t* out = args.a.out + ((int64_t)b * kv.Hq + head0 + row) * D;
-        if (!E4M3) {
+    for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-          for (int n = 0; n < D / 8; n++)
-            *reinterpret_cast<uint32_t*>(out + n * 8 + j2) = bf16x2(o[n][2 * r] * inv, o[n][2 * r + 1] * inv);
+      for (int i = 0; i < 2; i++) {
+        float sum = l[nb][i];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int row = 8 * nb + j2 + i;
+        if (row >= n_rows) continue;
+        if (whole) {
+          const float inv = sum == 0.0f ? 0.0f : kv.v_scale / sum;
+          uint16_t* out = args.a.out + ((int64_t)b * kv.Hq + head0 + row) * D;
+#pragma unroll
+          for (int n = 0; n < D / 16; n++) {
+            const uint32_t y = bf16x2(o[n][nb][i] * inv, o[n][nb][2 + i] * inv);
+            if (E4M3) {
+              *reinterpret_cast<uint32_t*>(out + n * 16 + 2 * g) = y;
+            } else {
+              out[n * 16 + g] = (uint16_t)y;
+              out[n * 16 + g + 8] = (uint16_t)(y >> 16);
+            }
+          }
+          if (g == 0) {
+            const float lse2 = sum == 0.0f ? kNegInf : m[nb][i] + log2f(sum);
+            if (args.a.lse) args.a.lse[(int64_t)b * kv.Hq + head0 + row] = lse2 * 0.6931471805599453f;
+            if (MASS) args.w.lse2[(int64_t)b * kv.Hq + head0 + row] = lse2;
+          }
         } else {
+          const int64_t at = ((int64_t)j * 2 + side) * kRows + row;
+          if (g == 0) args.w.ml[at] = make_float2(m[nb][i], sum);
+          float* po = args.w.o + at * D;
 #pragma unroll
-          for (int c = 0; c < D / 16; c++)
-            *reinterpret_cast<uint2*>(out + c * 16 + 2 * j2) =
-                make_uint2(bf16x2(o[2 * c][2 * r] * inv, o[2 * c + 1][2 * r] * inv),
-                           bf16x2(o[2 * c][2 * r + 1] * inv, o[2 * c + 1][2 * r + 1] * inv));
-        }
-        if ((lane & 3) == 0) {
-          const float lse2 = sum == 0.0f ? kNegInf : m[r] + log2f(sum);
-          if (args.a.lse) args.a.lse[(int64_t)b * kv.Hq + head0 + row] = lse2 * 0.6931471805599453f;
-          if (MASS) args.w.lse2[(int64_t)b * kv.Hq + head0 + row] = lse2;
-        }
-      } else {
-        const int64_t at = ((int64_t)j * 2 + part) * kRows + row;
-        if ((lane & 3) == 0) args.w.ml[at] = make_float2(m[r], sum);
-        float* po = args.w.o + at * D;
-        if (!E4M3) {
-#pragma unroll
-          for (int n = 0; n < D / 8; n++)
-            *reinterpret_cast<float2*>(po + n * 8 + j2) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < D / 16; c++)
-            *reinterpret_cast<float4*>(po + c * 16 + 2 * j2) =
-                make_float4(o[2 * c][2 * r], o[2 * c + 1][2 * r], o[2 * c][2 * r + 1], o[2 * c + 1][2 * r + 1]);
+          for (int n = 0; n < D / 16; n++) {
+            if (E4M3) {
+              *reinterpret_cast<float2*>(po + n * 16 + 2 * g) = make_float2(o[n][nb][i], o[n][nb][2 + i]);
+            } else {
+              po[n * 16 + g] = o[n][nb][i];
+              po[n * 16 + g + 8] = o[n][nb][2 + i];
+            }
+          }
         }
       }
-    }
   };
 
-  const uint32_t k_lane = E4M3 ? (lane & 15) * R::kStride + (lane >> 4) * 16
-                               : ((lane & 7) + ((lane >> 4) << 3)) * R::kStride + ((lane >> 3) & 1) * 16;
-  const uint32_t v_lane = (lane & 15) * R::kStride + (lane >> 4) * 16;
+  // ldmatrix addresses: lanes 0-7, 8-15, 16-23 and 24-31 point at the rows of the four
+  // 8 x 8 matrices, by halves of the entries first, or (values of a BF16 cache) of the
+  // dims.  `column` 16-byte pieces from the row's begin; the swizzle flips the piece's low
+  // bits by the row's.
+  constexpr uint32_t kFlip = R::kBox == 128 ? 7 : R::kBox == 64 ? 3 : 1, kFlipShift = R::kBox == 128 ? 0 : R::kBox == 64 ? 1 : 2;
+  const uint32_t row_e = lane & 15, col_e = lane >> 4, row_d = (lane & 7) + ((lane >> 4) << 3), col_d = (lane >> 3) & 1;
+  const uint32_t by_entry = row_e * R::kBox + ((col_e ^ ((row_e >> kFlipShift) & kFlip)) << 4);
+  const uint32_t by_dim = row_d * R::kBox + ((col_d ^ ((row_d >> kFlipShift) & kFlip)) << 4);
+  // pieces c (even) and c + 1 of the 16 entries from 16t on
+  auto piece = [&](uint32_t base, int t, int c) {
+    return (base ^ (uint32_t)((c % kBoxPieces) << 4)) + (uint32_t)((c / kBoxPieces) * R::kBoxBytes + t * 16 * R::kBox);
+  };
 
-  begin_row(cons.b, cons.hh);
-  int row_first = base + cons.hh * cons.nt;  // first tile of the row in the batch's order
-  Going going{-1, 0, 0, 0};
   int stage = 0;
+  uint32_t phase = 0;
+  bool broken = false;
+  bool fresh = true;  // a row begins with this tile
+#pragma unroll 1
   for (int at = lo; at < hi; at++) {
+    if (fresh) begin_row(cons.b, cons.hh);
     {
       const int ahead = stage + R::kStages - 1;
       load(ahead >= R::kStages ? ahead - R::kStages : ahead);
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(R::kStages - 1) : "memory");
-    __syncwarp();
+    if (!wait_full(full + stage, phase)) {
+      set_status(kv.status, kStTimeout);
+      broken = true;
+      break;
+    }
     const uint32_t k_at = ring32 + stage * R::kStage, v_at = k_at + R::kSide;
-    const int* rows = reinterpret_cast<const int*>(ring + stage * R::kStage + 2 * R::kSide);
-    const int2 ra = *reinterpret_cast<const int2*>(rows + j2), rb = *reinterpret_cast<const int2*>(rows + 8 + j2);
-    const int row_of[4] = {ra.x, ra.y, rb.x, rb.y};  // entries j2, j2+1, 8+j2, 9+j2 of the tile
+    const uint32_t there = there_of[stage];
+    if (there != kFull) {
+      // Values that no sequence wrote could be NaN, which no weight of zero makes zero.
+#pragma unroll 1
+      for (int i = lane; i < TILE * kPieces; i += 32) {
+        const int e = i / kPieces, c = i - e * kPieces;
+        if (!((there >> e) & 1u))
+          *reinterpret_cast<uint4*>(ring + stage * R::kStage + R::kSide + (c / kBoxPieces) * R::kBoxBytes + e * R::kBox +
+                                    (c % kBoxPieces) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a copy comes here again
+      __syncwarp();
+    }
 
-    float s[2][4] = {};
+    // The steps of a score go to KC sums in turn: products that wait for one another are few.
+    float part[KC][NT][NB][4];
+#pragma unroll
+    for (int c = 0; c < KC; c++)
+#pragma unroll
+      for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) part[c][t][nb][i] = 0.0f;
     if (!E4M3) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ks++) {
-        uint32_t b[4];
-        ldsm4(b, k_at + k_lane + ks * 32);
-        mma<false>(s[0], qf[ks], b[0], b[1]);
-        mma<false>(s[1], qf[ks], b[2], b[3]);
-      }
+      for (int ks = 0; ks < D / 16; ks++)
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+          uint32_t a[4];
+          ldsm4(a, k_at + piece(by_entry, t, 2 * ks));
+#pragma unroll
+          for (int nb = 0; nb < NB; nb++) mma<false>(part[ks % KC][t][nb], a, q[ks][nb]);
+        }
     } else {
 #pragma unroll
-      for (int k2 = 0; k2 < D / 32; k2++) {
-        uint32_t b[4];  // entries 0-7 and 8-15 of 16 dims, then of the next 16
-        ldsm4(b, k_at + k_lane + k2 * 32);
+      for (int k2 = 0; k2 < D / 32; k2++)
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-          mma<true>(s[0], qf[2 * k2 + u], e4m3x2_to_f16x2(b[2 * u]), e4m3x2_to_f16x2(b[2 * u] >> 16));
-          mma<true>(s[1], qf[2 * k2 + u], e4m3x2_to_f16x2(b[2 * u + 1]), e4m3x2_to_f16x2(b[2 * u + 1] >> 16));
+        for (int t = 0; t < NT; t++) {
+          uint32_t x[4];  // entries 0-7 and 8-15 of 16 dims, then of the next 16
+          ldsm4(x, k_at + piece(by_entry, t, 2 * k2));
+#pragma unroll
+          for (int u = 0; u < 2; u++) {
+            uint32_t a[4];
+            e4m3x4_to_f16(x[2 * u], a[0], a[2]);
+            e4m3x4_to_f16(x[2 * u + 1], a[1], a[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++) mma<true>(part[(2 * k2 + u) % KC][t][nb], a, q[2 * k2 + u][nb]);
+          }
         }
-      }
     }
 
-    // softmax step; lane rows g (and g + 8), four entries each
-    float p[NR][4];
-    bool moved = false;
-    float m_new[NR];
+    float s[NT][NB][4];
 #pragma unroll
-    for (int r = 0; r < NR; r++) {
+    for (int t = 0; t < NT; t++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float x = s[i >> 1][2 * r + (i & 1)] * qs[r];
-        p[r][i] = row_of[i] < 0 ? kNegInf : x;
-      }
-      if (MASS && g + 8 * r < n_rows) {
-        const int head = head0 - (cons.hh / args.groups) * kv.G + g + 8 * r;
+      for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-          if (row_of[i] >= 0)
-            args.w.scores[(((int64_t)(row_of[i] >> kv.page_shift) * kv.G + head) << kv.page_shift) +
-                          (row_of[i] & kv.page_mask)] = p[r][i];
-      }
-      float top = fmaxf(fmaxf(p[r][0], p[r][1]), fmaxf(p[r][2], p[r][3]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      m_new[r] = fmaxf(m[r], top);
-      moved |= m_new[r] != m[r];
-    }
-    if (__any_sync(0xffffffffu, moved)) {
+        for (int i = 0; i < 4; i++) {
+          s[t][nb][i] = part[0][t][nb][i];
 #pragma unroll
-      for (int r = 0; r < NR; r++) {
-        const float down = m_new[r] == m[r] ? 1.0f : exp2_fast(m[r] - m_new[r]);
-        l[r] *= down;
-#pragma unroll
-        for (int n = 0; n < D / 8; n++) {
-          o[n][2 * r] *= down;
-          o[n][2 * r + 1] *= down;
+          for (int c = 1; c < KC; c++) s[t][nb][i] += part[c][t][nb][i];
         }
-        m[r] = m_new[r];
-      }
-    }
-    uint32_t hi_p[4], lo_p[4];
+
+    // softmax step.  s[t][nb][2e + i]: entry 16t + 8e + g, head 8nb + j2 + i.
+    float top[NB][2];
+    bool over = false;
 #pragma unroll
-    for (int r = 0; r < NR; r++) {
-      const float zero = m[r] == kNegInf ? 0.0f : m[r];  // a row without a score yet: 2^(-inf) = 0
-#pragma unroll
-      for (int i = 0; i < 4; i++) p[r][i] = exp2_fast(p[r][i] - zero);
-      l[r] += (p[r][0] + p[r][1]) + (p[r][2] + p[r][3]);
+    for (int nb = 0; nb < NB; nb++)
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        const float x = p[r][2 * i], y = p[r][2 * i + 1];
-        if (E4M3) {
-          hi_p[2 * i + r] = f16x2(x, y);
-        } else {  // bf16 keeps 8 bits of p: the rest goes through a second product
-          const uint32_t u = bf16x2(x, y);
-          hi_p[2 * i + r] = u;
-          lo_p[2 * i + r] = bf16x2(x - bf16_lo(u), y - bf16_hi(u));
-        }
+        float x = kNegInf;
+#pragma unroll
+        for (int t = 0; t < NT; t++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const bool gone = there != kFull && !((there >> (16 * t + 8 * e + g)) & 1u);
+            s[t][nb][2 * e + i] = gone ? kNegInf : s[t][nb][2 * e + i] * qs[nb][i];
+            x = fmaxf(x, s[t][nb][2 * e + i]);
+          }
+        top[nb][i] = x;
+        over |= x > m[nb][i] + kSlack;
       }
+    if (MASS && at < args.w.tiles) {
+      float* sc = args.w.scores + (int64_t)at * (8 * NB * TILE) + j2 * TILE + g;
+#pragma unroll
+      for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) sc[(8 * nb + (i & 1)) * TILE + 16 * t + 8 * (i >> 1)] = s[t][nb][i];
     }
-    if (NR == 1) hi_p[1] = hi_p[3] = lo_p[1] = lo_p[3] = 0u;
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          float x = top[nb][i];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x = fmaxf(x, m[nb][i]);
+          const float down = x == m[nb][i] ? 1.0f : exp2_fast(m[nb][i] - x);
+          m[nb][i] = x;
+          l[nb][i] *= down;
+#pragma unroll
+          for (int n = 0; n < D / 16; n++) {
+            o[n][nb][i] *= down;
+            o[n][nb][2 + i] *= down;
+          }
+        }
+    }
+    uint32_t hi_p[NT][NB][2], lo_p[NT][NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; nb++) {
+      const float z0 = m[nb][0] == kNegInf ? 0.0f : m[nb][0];  // a row without a score yet: 2^(-inf) = 0
+      const float z1 = m[nb][1] == kNegInf ? 0.0f : m[nb][1];
+#pragma unroll
+      for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const float x = exp2_fast(s[t][nb][2 * e] - z0), y = exp2_fast(s[t][nb][2 * e + 1] - z1);
+          l[nb][0] += x;
+          l[nb][1] += y;
+          if (E4M3) {
+            hi_p[t][nb][e] = transposed(f16x2(x, y));
+          } else {  // bf16 keeps 8 bits of p: the rest goes through a second product
+            const uint32_t u = bf16x2(x, y);
+            hi_p[t][nb][e] = transposed(u);
+            lo_p[t][nb][e] = transposed(bf16x2(x - bf16_lo(u), y - bf16_hi(u)));
+          }
+        }
+    }
 
     if (!E4M3) {
 #pragma unroll
-      for (int n = 0; n < D / 16; n++) {
-        uint32_t b[4];
-        ldsm4t(b, v_at + v_lane + n * 32);
-        mma<false>(o[2 * n], hi_p, b[0], b[1]);
-        mma<false>(o[2 * n + 1], hi_p, b[2], b[3]);
-        mma<false>(o[2 * n], lo_p, b[0], b[1]);
-        mma<false>(o[2 * n + 1], lo_p, b[2], b[3]);
-      }
+      for (int n = 0; n < D / 16; n++)
+#pragma unroll
+        for (int t = 0; t < NT; t++) {
+          uint32_t a[4];
+          ldsm4t(a, v_at + piece(by_dim, t, 2 * n));
+#pragma unroll
+          for (int nb = 0; nb < NB; nb++) {
+            mma<false>(o[n][nb], a, hi_p[t][nb]);
+            mma<false>(o[n][nb], a, lo_p[t][nb]);
+          }
+        }
     } else {
 #pragma unroll
-      for (int n = 0; n < D / 32; n++) {
-        uint32_t b[4];  // entries 0-7 and 8-15 of 16 dims, then of the next 16
-        ldsm4t(b, v_at + v_lane + n * 32);
+      for (int n = 0; n < D / 32; n++)
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-          const uint32_t x = __byte_perm(b[2 * u], 0, 0x3120), y = __byte_perm(b[2 * u + 1], 0, 0x3120);
-          mma<true>(o[4 * n + 2 * u], hi_p, e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(y));
-          mma<true>(o[4 * n + 2 * u + 1], hi_p, e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y >> 16));
+        for (int t = 0; t < NT; t++) {
+          uint32_t x[4];  // entries 0-7 and 8-15 of 16 dims, then of the next 16
+          ldsm4t(x, v_at + piece(by_entry, t, 2 * n));
+#pragma unroll
+          for (int u = 0; u < 2; u++) {
+            uint32_t a[4];
+            e4m3x4_to_f16(__byte_perm(x[2 * u], 0, 0x3120), a[0], a[1]);
+            e4m3x4_to_f16(__byte_perm(x[2 * u + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+            for (int nb = 0; nb < NB; nb++) mma<true>(o[2 * n + u][nb], a, hi_p[t][nb]);
+          }
         }
-      }
     }
     __syncwarp();  // the stage may be loaded again
-    stage = stage + 1 == R::kStages ? 0 : stage + 1;
+    if (++stage == R::kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
 
     const bool last = cons.t + 1 == cons.nt;
     if (last || at + 1 == hi) {
-      const bool whole = last && row_first >= lo;
-      end_row(cons.b, whole, row_first >= lo ? 1 : 0);
+      end_row(cons.b, last && row_first >= lo, row_first >= lo ? 1 : 0);
       if (!last) {
-        const int j0 = row_first / chunk;
-        going = Going{cons.b, cons.hh, j0, (row_first + cons.nt - 1) / chunk - j0 + 1};
+        left.go_b = cons.b;
+        left.go_hh = cons.hh;
+        left.go_j0 = row_first / chunk;
+        left.go_parts = (row_first + cons.nt - 1) / chunk - left.go_j0 + 1;
       }
       row_first += cons.nt;
-      if (at + 1 < hi) {
-        advance(kv, cons, items);
-        begin_row(cons.b, cons.hh);
-      }
+      if (at + 1 < hi) advance<TILE>(kv, cons, items);
+      fresh = true;
     } else {
       cons.t++;
+      fresh = false;
     }
   }
-  if (lane == 0) args.w.going[j] = going;
+  if (broken) {  // the copies still under way land before the block leaves
+    for (int i = 1; i < R::kStages; i++) {
+      if (++stage == R::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (i < R::kStages) wait_full(full + stage, phase);
+    }
+    left.tiles = 0;
+    left.go_b = -1;
+  }
+  if (lane == 0) args.w.chunks[j] = left;
+  if (MASS && lane == 0 && hi > args.w.tiles) set_status(kv.status, kStBadId);
 }
 
 // ---------------------------------------------------------------------------
 // join: block j serves the row that goes on past the end of chunk j.  The P
-// parts of a row lie on the chunks j0 .. j0+P-1, so P - 1 blocks share its
-// units (one query head x 32 dims): a row in many parts has many blocks.
+// parts of a row lie on the chunks j0 .. j0+P-1, so P - 1 blocks share it: a row
+// in many parts has many blocks.  Part p lies on chunk j0 + p, side 1 (the row
+// begins) for p = 0, else side 0.
+//
+// With MASS block j then adds the weights of chunk j's entries: 2^(score - lse)
+// over the query heads of their KV head.
 // ---------------------------------------------------------------------------
 struct JoinArgs {
   KvAttnArgs a;
   AttnWork w;
   int groups;
-  int D;
-  bool mass;
 };
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = 128;   // 8 threads for the statistics of each of 16 rows
+constexpr int kJoinWarps = kJoinThreads / 32;
 
-__device__ __forceinline__ float part_weight(float m, float top) { return m == kNegInf ? 0.0f : exp2_fast(m - top); }
-
-__global__ void __launch_bounds__(kJoinWarps * 32) k_kv_join(JoinArgs args) {
-  __shared__ float s_acc[kJoinWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const KvView& kv = args.a.kv;
-  kv_pdl_trigger();
-  kv_pdl_wait();
-  const Going gg = args.w.going[blockIdx.x];
-  if (gg.b < 0) return;
-  const int h = gg.hh / args.groups, gi = gg.hh - h * args.groups;
-  const int n_rows = min(kRows, kv.G - gi * kRows), head0 = h * kv.G + gi * kRows;
-  const int dims = args.D >> 5, units = n_rows * dims;
-  const int parts = gg.parts, blocks = parts - 1, mine = (int)blockIdx.x - gg.j0;
-  // Several units for this block: a warp each.  Else its warps share a unit's parts.
-  const bool shared = units <= blocks * 4;
-  for (int u = shared ? mine : mine + blocks * warp; u < units; u += shared ? blocks : blocks * kJoinWarps) {
-    const int row = u / dims, dim = (u - row * dims) * 32 + lane;
-    // part p lies on chunk j0 + p: side 1 (the row begins) for p = 0, else side 0
-    auto slot = [&](int p) { return ((int64_t)(gg.j0 + p) * 2 + (p == 0 ? 1 : 0)) * kRows + row; };
-    float top = kNegInf;
-    for (int p = lane; p < parts; p += 32) top = fmaxf(top, args.w.ml[slot(p)].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    float sum = 0.0f;
-    for (int p = lane; p < parts; p += 32) {
-      const float2 ml = args.w.ml[slot(p)];
-      sum += ml.x == kNegInf ? ml.y : ml.y * exp2_fast(ml.x - top);  // no score: l is 0, or NaN
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    float acc = 0.0f;
+// m and l of the rows of an item over their parts, by 8 threads a row.
+__device__ __forceinline__ void join_ml(const float2* ml, int j0, int parts, float2* s_ml) {
+  const int row = threadIdx.x >> 3, sub = threadIdx.x & 7;
+  float top = kNegInf, sum = 0.0f;
+  auto add = [&](float2 x) {  // a part without a score: l is 0, or NaN
+    const float both = fmaxf(top, x.x);
+    sum = (top == both ? sum : sum * exp2_fast(top - both)) + (x.x == both || x.x == kNegInf ? x.y : x.y * exp2_fast(x.x - both));
+    top = both;
+  };
 #pragma unroll 4
-    for (int p = shared ? warp : 0; p < parts; p += shared ? kJoinWarps : 1) {
-      const int64_t at = slot(p);
-      acc += part_weight(args.w.ml[at].x, top) * args.w.o[at * args.D + dim];
-    }
-    if (shared) {
-      s_acc[warp][lane] = acc;
-      __syncthreads();
-      if (warp == 0) {
-        acc = 0.0f;
+  for (int p = sub; p < parts; p += 8) add(ml[((int64_t)(j0 + p) * 2 + (p == 0 ? 1 : 0)) * kRows + row]);
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; w++) acc += s_acc[w][lane];
-      }
-      __syncthreads();
-      if (warp != 0) continue;
-    }
-    const int64_t head = (int64_t)gg.b * kv.Hq + head0 + row;
-    const __nv_bfloat16 y = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc * (kv.v_scale / sum));
-    args.a.out[head * args.D + dim] = *reinterpret_cast<const uint16_t*>(&y);
-    if (dim == 0) {
-      const float lse2 = sum == 0.0f ? kNegInf : top + log2f(sum);
-      if (args.a.lse) args.a.lse[head] = lse2 * 0.6931471805599453f;
-      if (args.mass) args.w.lse2[head] = lse2;
-    }
+  for (int d = 4; d > 0; d >>= 1) {
+    const float2 x = make_float2(__shfl_xor_sync(0xffffffffu, top, d), __shfl_xor_sync(0xffffffffu, sum, d));
+    add(x);
   }
+  if (sub == 0) s_ml[row] = make_float2(top, sum);
 }
 
-// ---------------------------------------------------------------------------
-// mass: block j walks chunk j's tiles again, two a warp (a half warp each), and
-// adds 2^(score - lse) over the query heads of the KV head.
-// ---------------------------------------------------------------------------
-constexpr int kMassThreads = 128;
-
-__global__ void __launch_bounds__(kMassThreads) k_kv_mass(JoinArgs args) {
+template <int D, int TILE, bool MASS>
+__global__ void __launch_bounds__(kJoinThreads, 8) k_kv_join(JoinArgs args) {
+  __shared__ float2 s_ml[kRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const KvView& kv = args.a.kv;
   kv_pdl_wait();
-  const int4 st = args.w.start[blockIdx.x];
-  if (st.x < 0) return;
-  const int items = kv.Hkv * args.groups;
-  Place p{st.x, st.y, st.z, kv_length(kv, st.x), 0};
-  p.nt = tiles_of(p.len);
-  const int e = threadIdx.x & 15;
-  int skip = threadIdx.x >> 4;
-  for (int i = skip; i < st.w; i += kMassThreads / 16, skip = kMassThreads / 16) {
-    p.t += skip;
-    while (p.t >= p.nt) {
-      p.t -= p.nt;
-      if (++p.hh == items) {
-        p.hh = 0;
-        next_sequence(kv, p);
+  const Chunk c = args.w.chunks[blockIdx.x];
+  if (blockIdx.y == 0) {
+    if (c.go_b < 0) return;
+    const int h = c.go_hh / args.groups, gi = c.go_hh - h * args.groups;
+    const int n_rows = min(kRows, kv.G - gi * kRows);
+    const int64_t head0 = (int64_t)c.go_b * kv.Hq + h * kv.G + gi * kRows;
+    const int j0 = c.go_j0, parts = c.go_parts, blocks = parts - 1, mine = (int)blockIdx.x - j0;
+    join_ml(args.w.ml, j0, parts, s_ml);  // rows above n_rows: whatever memory held, not used
+    __syncthreads();
+    if (mine == 0 && tid < n_rows && args.a.lse)
+      args.a.lse[head0 + tid] = s_ml[tid].y == 0.0f ? kNegInf : (s_ml[tid].x + log2f(s_ml[tid].y)) * 0.6931471805599453f;
+    // Units of four dims of a row.  `split` lanes share a unit's parts while
+    // there are more threads than units.
+    const int units = n_rows * (D / 4), threads = blocks * kJoinThreads;
+    int split = 1;
+    while (split < 32 && split * 2 <= parts && units * split * 2 <= threads) split *= 2;
+    const int width = 32 / split;
+    for (int u0 = (mine * kJoinWarps + warp) * width; u0 < units; u0 += blocks * kJoinWarps * width) {
+      const int u = min(u0 + lane % width, units - 1), row = u / (D / 4), d4 = u - row * (D / 4);
+      const float2 ml = s_ml[row];
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int p = lane / width; p < parts; p += split) {
+        const int64_t at = ((int64_t)(j0 + p) * 2 + (p == 0 ? 1 : 0)) * kRows + row;
+        const float m = args.w.ml[at].x;
+        const float4 x = *reinterpret_cast<const float4*>(args.w.o + at * D + d4 * 4);
+        const float w = m == kNegInf ? 0.0f : exp2_fast(m - ml.x);
+        acc.x += w * x.x;
+        acc.y += w * x.y;
+        acc.z += w * x.z;
+        acc.w += w * x.w;
+      }
+      for (int d = width; d < 32; d <<= 1) {
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, d);
+        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, d);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, d);
+        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, d);
+      }
+      const float inv = ml.y == 0.0f ? 0.0f : kv.v_scale / ml.y;
+      if (lane < width && u0 + lane < units)
+        *reinterpret_cast<uint2*>(args.a.out + (head0 + row) * D + d4 * 4) =
+            make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+    }
+    return;
+  }
+  if (!MASS || c.tiles == 0) return;
+
+  const int items = kv.Hkv * args.groups, rows_kept = kv.G > 8 ? 16 : 8;
+  const int lo = (int)blockIdx.x * c.size, hi = lo + c.tiles;
+  Place p{c.b, c.hh, 0, c.len, tiles_of<TILE>(c.len)};
+  for (int first = c.first; first < hi;) {
+    const int h = p.hh / args.groups;
+    if (p.hh == h * args.groups) {  // the first group's tiles stand for the entries; all groups are added there
+      const int t0 = max(lo, first) - first, t1 = min(hi, first + p.nt) - first;
+      for (int gi = 0; gi < args.groups; gi++) {
+        const int row_first = first + gi * p.nt, j0 = row_first / c.size;
+        const int parts = (row_first + p.nt - 1) / c.size - j0 + 1, n_rows = min(kRows, kv.G - gi * kRows);
+        __syncthreads();
+        if (parts == 1) {  // written as m = lse, l = 1
+          if (tid < n_rows) s_ml[tid] = make_float2(args.w.lse2[(int64_t)p.b * kv.Hq + h * kv.G + gi * kRows + tid], 1.0f);
+        } else {
+          join_ml(args.w.ml, j0, parts, s_ml);
+        }
+        __syncthreads();
+        if (tid < n_rows) s_ml[tid].x = s_ml[tid].y == 0.0f ? kNegInf : s_ml[tid].x + log2f(s_ml[tid].y);
+        __syncthreads();
+        // four entries a thread
+        for (int e = t0 * TILE + tid * 4; e < min(t1 * TILE, p.len); e += kJoinThreads * 4) {
+          const int64_t tile = row_first + e / TILE;
+          if (tile >= args.w.tiles) break;
+          const float* sc = args.w.scores + tile * rows_kept * TILE + e % TILE;
+          float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+          for (int r = 0; r < n_rows; r++) {
+            const float z = s_ml[r].x;
+            const float4 x = *reinterpret_cast<const float4*>(sc + r * TILE);
+            if (z == kNegInf) continue;  // no weight anywhere
+            sum.x += exp2_fast(x.x - z);
+            sum.y += exp2_fast(x.y - z);
+            sum.z += exp2_fast(x.z - z);
+            sum.w += exp2_fast(x.w - z);
+          }
+          const float add[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int row = e + i < p.len ? kv_row(kv, p.b, h, e + i) : -1;
+            if (row >= 0) kv.mass[row] += add[i];
+          }
+        }
       }
     }
-    const int h = p.hh / args.groups;
-    const int slot = p.t * kTile + e;
-    if (p.hh != h * args.groups || slot >= p.len) continue;  // the first group adds all heads of h
-    const int row = kv_row(kv, p.b, h, slot);
-    if (row < 0) continue;
-    const float* sc = args.w.scores + (((int64_t)(row >> kv.page_shift) * kv.G) << kv.page_shift) + (row & kv.page_mask);
-    const float* lse2 = args.w.lse2 + (int64_t)p.b * kv.Hq + h * kv.G;
-    float sum = 0.0f;
-#pragma unroll 8
-    for (int g = 0; g < kv.G; g++) {
-      const float z = lse2[g];
-      sum += z == kNegInf ? 0.0f : exp2_fast(sc[(int64_t)g << kv.page_shift] - z);
+    first += p.nt;
+    if (first < hi) {
+      p.t = p.nt - 1;
+      advance<TILE>(kv, p, items);
     }
-    kv.mass[row] += sum;
   }
 }
 
-template <int D, bool E4M3, bool WIDE, bool MASS>
-cudaError_t run(const SplitArgs& a, int sms, cudaStream_t s) {
+template <int D, bool E4M3, int NB, bool MASS>
+cudaError_t run(SplitArgs& a, int sms, cudaStream_t s) {
   using R = Ring<D * (E4M3 ? 1 : 2)>;
   static_assert(R::kStages >= 2 && R::kWarps <= kMaxWarps, "a ring of at least two stages fits");
-  auto kern = k_kv_split<D, E4M3, WIDE, MASS>;
+  static_assert(R::kTile == tile_of(D * (E4M3 ? 1 : 2)), "the workspace is carved for this tile");
+  const KvView& kv = a.a.kv;
+  const uint64_t rows = (uint64_t)kv.n_pages * kv.Hkv << kv.page_shift;
+  a.box_shift = R::kTile == 32 ? 5 : 4;
+  if (kv.page_shift < a.box_shift) a.box_shift = kv.page_shift;
+  if (encode_tmap_rows(&a.k_map, kv.k, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift) != FT_OK ||
+      encode_tmap_rows(&a.v_map, kv.v, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift) != FT_OK)
+    return cudaErrorInvalidValue;
+  auto kern = k_kv_split<D, E4M3, NB, MASS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
   if (e != cudaSuccess) return e;
   kern<<<sms, R::kWarps * 32, R::kBytes, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const JoinArgs ja{a.a, a.w, a.groups, D, MASS};
-  const dim3 chunks((unsigned)(sms * R::kWarps));
-  if ((e = kv_launch_after(k_kv_join, chunks, kJoinWarps * 32, 0, s, ja)) != cudaSuccess) return e;
-  return MASS ? kv_launch_after(k_kv_mass, chunks, kMassThreads, 0, s, ja) : cudaSuccess;
+  const JoinArgs ja{a.a, a.w, a.groups};
+  // The same split of the SMs' memory as the kernel before it: no SM has to change over between the two.
+  auto join = k_kv_join<D, R::kTile, MASS>;
+  e = cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return e;
+  return kv_launch_after(join, dim3((unsigned)(sms * R::kWarps), MASS ? 2 : 1), kJoinThreads, 0, s, ja);
 }
 
 template <int D, bool E4M3>
-cudaError_t run_d(const SplitArgs& a, int sms, cudaStream_t s) {
-  if (a.a.kv.G > 8) return a.a.mass ? run<D, E4M3, true, true>(a, sms, s) : run<D, E4M3, true, false>(a, sms, s);
-  return a.a.mass ? run<D, E4M3, false, true>(a, sms, s) : run<D, E4M3, false, false>(a, sms, s);
+cudaError_t run_d(SplitArgs& a, int sms, cudaStream_t s) {
+  if (a.a.kv.G > 8) return a.a.mass ? run<D, E4M3, 2, true>(a, sms, s) : run<D, E4M3, 2, false>(a, sms, s);
+  return a.a.mass ? run<D, E4M3, 1, true>(a, sms, s) : run<D, E4M3, 1, false>(a, sms, s);
 }
 
 }  // namespace
 
 int64_t kv_attn_workspace(const ft_kv_cache& c) {
   AttnWork w;
-  return carve(w, nullptr, c.head_dim, c.n_seqs, c.n_heads, c.mass ? c.n_pages * c.n_kv_heads * c.page_size : 0,
-               c.n_heads / c.n_kv_heads);
+  return carve(w, nullptr, c.head_dim, c.head_dim * (c.format == FT_KV_E4M3 ? 1 : 2), c.n_seqs, c.n_heads, c.n_kv_heads,
+               c.n_pages * c.n_kv_heads * c.page_size, c.mass != nullptr);
 }
 
 cudaError_t launch_kv_attention(const KvAttnArgs& args, bool e4m3, int sms, cudaStream_t s) {
@@ -704,7 +898,8 @@ cudaError_t launch_kv_attention(const KvAttnArgs& args, bool e4m3, int sms, cuda
   a.a = args;
   a.groups = (args.kv.G + kRows - 1) / kRows;
   const KvView& kv = args.kv;
-  carve(a.w, args.work, kv.D, kv.n_seqs, kv.Hq, 0, kv.G);
+  carve(a.w, args.work, kv.D, kv.D * (e4m3 ? 1 : 2), kv.n_seqs, kv.Hq, kv.Hkv,
+        (int64_t)kv.n_pages * kv.Hkv << kv.page_shift, args.mass);
   sms = sms < kKvMaxSms ? sms : kKvMaxSms;
   switch (kv.D) {
     case 64: return e4m3 ? run_d<64, true>(a, sms, s) : run_d<64, false>(a, sms, s);

@@ -561,7 +561,7 @@ typedef struct {
   int32_t head_dim;      /* D: 64, 96, 128, 192 or 256 */
   int32_t n_heads;       /* query heads, a multiple of n_kv_heads; the heads h*G .. h*G+G-1 share KV head h */
   int32_t n_kv_heads;
-  int32_t page_size;     /* entries of a page: a power of two from 1 to 1024 */
+  int32_t page_size;     /* entries of a page: a power of two from 8 to 1024 */
   int32_t n_seqs;        /* rows of block_table and lengths, at most 65536 (0: every call is a no-op) */
   int32_t max_pages;     /* columns of block_table; max_pages * page_size <= 2^30 */
   int64_t n_pages;       /* pages of the pools; n_pages * n_kv_heads * page_size < 2^31 */
@@ -574,7 +574,7 @@ typedef struct {
   int32_t* pos;          /* dev int32, the same shape: the token's position on axis 0, or NULL */
   const int32_t* block_table; /* dev int32 [n_seqs][max_pages] */
   int32_t* lengths;      /* dev int32 [n_seqs] */
-  int32_t* status;       /* dev int32: device-detected errors are OR-ed into it (bit 2); NULL drops them */
+  int32_t* status;       /* dev int32: device-detected errors are OR-ed into it; NULL drops them */
 } ft_kv_cache;
 
 #define FT_KV_BF16 0
@@ -659,7 +659,8 @@ FT_API ft_status ft_kv_evict(const ft_kv_cache* kv, const int32_t* budgets, int3
                              int64_t workspace_bytes, void* stream);
 
 /* Copy the cache's status word to the host (synchronising `stream`), clear
- * it, and map it: bad contents -> FT_ERR_INVALID; else FT_OK (also without a
+ * it, and map it: a bounded wait inside a kernel that gave up (bit 4) ->
+ * FT_ERR_TIMEOUT, bad contents -> FT_ERR_INVALID; else FT_OK (also without a
  * status word). */
 FT_API ft_status ft_kv_sync_status(const ft_kv_cache* kv, void* stream);
 

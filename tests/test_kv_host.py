@@ -48,7 +48,7 @@ def evict(kv=None, **kw):
 SHAPES = [
     (dict(head_dim=80), "head_dim"), (dict(head_dim=0), "head_dim"), (dict(n_kv_heads=0), "n_heads"),
     (dict(n_heads=0), "n_heads"), (dict(n_heads=9), "n_heads"), (dict(n_heads=131072), "n_heads"),
-    (dict(page_size=0), "page_size"), (dict(page_size=24), "page_size"), (dict(page_size=2048), "page_size"),
+    (dict(page_size=0), "page_size"), (dict(page_size=4), "page_size"), (dict(page_size=24), "page_size"), (dict(page_size=2048), "page_size"),
     (dict(n_seqs=-1), "n_seqs"), (dict(n_seqs=65537), "n_seqs"), (dict(max_pages=0), "max_pages"),
     (dict(max_pages=1 << 27), "max_pages"), (dict(n_pages=0), "n_pages"), (dict(n_pages=1 << 26), "n_pages"),
     (dict(n_seqs=65536, max_pages=1 << 14), "too large"), (dict(format=2), "format"), (dict(format=-1), "format"),
