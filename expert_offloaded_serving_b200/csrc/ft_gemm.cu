@@ -459,17 +459,17 @@ ft_status encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t inner_byte
 }
 
 ft_status encode_tmap_rows(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_bytes,
-                           uint32_t box_rows) {
+                           uint32_t box_rows, uint32_t box_columns) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return FT_ERR_CUDA;
-  cuuint64_t dims[2] = {row_bytes, rows};
-  cuuint64_t strides[1] = {row_bytes};
-  cuuint32_t box[2] = {box_bytes, box_rows};
-  cuuint32_t es[2] = {1, 1};
+  cuuint64_t dims[3] = {box_bytes, rows, row_bytes / box_bytes};
+  cuuint64_t strides[2] = {row_bytes, box_bytes};
+  cuuint32_t box[3] = {box_bytes, box_rows, box_columns};
+  cuuint32_t es[3] = {1, 1, 1};
   const CUtensorMapSwizzle swizzle = box_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                                      : box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                        : CU_TENSOR_MAP_SWIZZLE_32B;
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FT_OK : FT_ERR_CUDA;

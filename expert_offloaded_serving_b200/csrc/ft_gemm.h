@@ -57,9 +57,10 @@ struct GemmMaps {
 ft_status encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows, uint64_t depth,
                          uint64_t row_pitch, uint64_t depth_pitch);
 ft_status encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t inner_bytes, uint64_t rows, uint64_t row_pitch);
-// Dense rows, boxes of box_bytes (32, 64 or 128, swizzled over as much) x box_rows.
+// Dense rows cut into columns of box_bytes (32, 64 or 128, swizzled over as
+// much): (box_bytes, rows, columns) 3-D, boxes of box_rows x box_columns.
 ft_status encode_tmap_rows(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_bytes,
-                           uint32_t box_rows);
+                           uint32_t box_rows, uint32_t box_columns);
 
 size_t gemm_smem_bytes(int mode, int fmt);
 cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& maps, cudaStream_t s);

@@ -50,8 +50,8 @@ ft_status check_shape(const ft_kv_cache* c) {
   if (c->n_pages < 1 || c->n_pages >= ((int64_t)1 << 31) / rows_a_page)
     return refuse(FT_ERR_INVALID, "n_pages %lld: the pools hold 1 page to 2^31 - 1 rows", (long long)c->n_pages);
   const int64_t groups = (c->n_heads / c->n_kv_heads + 15) / 16, tiles = ((int64_t)c->max_pages * c->page_size + 15) / 16;
-  if ((double)c->n_seqs * (double)tiles * (double)(c->n_kv_heads * groups) >= 2147483648.0)
-    return refuse(FT_ERR_INVALID, "n_seqs x max_pages x heads is too large: 2^31 tiles of 16 entries at most");
+  if ((double)c->n_seqs * (double)tiles * (double)(c->n_kv_heads * groups) >= 1073741824.0)
+    return refuse(FT_ERR_INVALID, "n_seqs x max_pages x heads is too large: below 2^30 tiles of 16 entries");
   if (c->format != FT_KV_BF16 && c->format != FT_KV_E4M3)
     return refuse(FT_ERR_INVALID, "format %d is not FT_KV_BF16 or FT_KV_E4M3", c->format);
   if (!(c->k_scale > 0) || !(c->v_scale > 0) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))

@@ -92,10 +92,11 @@ cudaError_t launch_kv_attention(const KvAttnArgs& a, bool e4m3, int sms, cudaStr
 cudaError_t launch_kv_evict(const KvEvictArgs& a, int row_bytes, int sms, cudaStream_t s);
 
 // Launch with programmatic stream serialisation: the kernel may start while
-// its predecessor on the stream still runs, and reads nothing that one wrote
-// before its own griddepcontrol.wait.
+// its predecessor on the stream still runs.  Every thread of every kernel here executes
+// griddepcontrol.wait before it touches memory that another kernel may have
+// written or still reads, so a grid ends only after all those before it.
 template <typename A>
-inline cudaError_t kv_launch_after(void (*kern)(A), dim3 grid, int threads, size_t smem, cudaStream_t s, const A& a) {
+inline cudaError_t kv_launch_after(void (*kern)(const A), dim3 grid, int threads, size_t smem, cudaStream_t s, const A& a) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);

@@ -79,7 +79,7 @@ struct AttnWork {
   float2* ml;        // [chunks][2][16] m and l of a part (log2 units); side 0: a row that came in, 1: one that goes on
   float* o;          // [chunks][2][16][D]
   float* lse2;       // [n_seqs][Hq] lse of whole rows in log2 units (mass)
-  float* scores;     // [tiles][8 or 16 rows][entries of a tile] scores in log2 units (mass)
+  float* scores;     // [tiles][entries of a tile][8 or 16 rows] scores in log2 units (mass)
   int64_t tiles;     // that `scores` holds
 };
 
@@ -107,10 +107,11 @@ inline int64_t carve(AttnWork& w, uint8_t* base, int D, int row_bytes, int n_seq
 }
 
 struct SplitArgs {
-  CUtensorMap k_map, v_map;  // rows of the pools, boxes of kBox bytes x box_rows
+  CUtensorMap k_map, v_map;  // pools as kBox bytes x rows x kBoxes; a box has box_rows, and all kBoxes where that is a tile's rows
   KvAttnArgs a;
   AttnWork w;
   int groups;     // items of a KV head: groups of 16 query heads
+  float per_warp;  // 1 / warps of the launch
   int box_shift;  // box_rows = 1 << box_shift: a tile's rows, or a page's where pages are smaller
 };
 
@@ -254,13 +255,67 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = kv.Hkv * args.groups;
 
-  kv_pdl_trigger();
   uint64_t* const full = s_full + warp * R::kStages;
   if (lane < R::kStages) tc::mbar_init(full + lane, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  // Tiles of the batch and where each thread's share of the sequences begins.
-  const int per = (kv.n_seqs + kThreads - 1) / kThreads;
-  {
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&args.k_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&args.v_map) : "memory");
+  }
+  kv_pdl_wait();
+  kv_pdl_trigger();
+  const int j = warp * gridDim.x + blockIdx.x;  // neighbours in the batch sit on different SMs
+  const int warps = (int)gridDim.x * R::kWarps;
+  auto chunk_of = [&](int total) {  // ceil(total / warps), exact: the estimate is at most one off
+    int n = (int)((float)total * args.per_warp);
+    n += n * warps < total;
+    n += n * warps < total;
+    n -= (n - 1) * warps >= total && n > 0;
+    return max(kMinEntries / TILE, n);
+  };
+  // The tiles of the batch are counted, cut, and the chunk's first one is looked up: its
+  // sequence, and that one's first tile in the batch.
+  Place cons;
+  int base, total, chunk, lo, hi;
+  auto cut = [&] {
+    chunk = chunk_of(total);
+    lo = (int)min((int64_t)j * chunk, (int64_t)total);
+    hi = min(lo + chunk, total);
+  };
+  if (kv.n_seqs <= 128) {  // every warp by itself, four sequences a lane
+    int len[4], upto[4];  // tiles up to and with the lane's sequence
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int b = i * 32 + lane;
+      len[i] = b < kv.n_seqs ? kv_length(kv, b, blockIdx.x == 0 && warp == 0) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      upto[i] = total;
+      if (i * 32 >= kv.n_seqs) continue;
+      int run = tiles_of<TILE>(len[i]) * items;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, run, d);
+        if (lane >= d) run += x;
+      }
+      upto[i] += run;
+      total = __shfl_sync(0xffffffffu, upto[i], 31);
+    }
+    cut();
+    cons.b = cons.len = base = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; i--) {
+      // sequences of these 32 whose tiles all lie before the chunk; one holds `lo` if not all do
+      const int before = __popc(__ballot_sync(0xffffffffu, upto[i] <= lo));
+      if (i * 32 >= kv.n_seqs || before == 32) continue;
+      cons.b = i * 32 + before;
+      cons.len = __shfl_sync(0xffffffffu, len[i], before);
+      base = __shfl_sync(0xffffffffu, upto[i], before) - tiles_of<TILE>(cons.len) * items;
+    }
+  } else {  // the block together: a run of `per` sequences a thread
+    const int per = (kv.n_seqs + kThreads - 1) / kThreads;
     int sum = 0;
     for (int i = 0; i < per; i++) {
       const int b = tid * per + i;
@@ -278,47 +333,42 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     s_sum[tid + 1] = run;
     if (tid == 0) s_sum[0] = 0;
     __syncthreads();
-  }
-  // Idle rows: out 0, lse -inf.
-  for (int b = blockIdx.x; b < kv.n_seqs; b += gridDim.x) {
-    if (kv_length(kv, b) != 0) continue;
-    uint32_t* o = reinterpret_cast<uint32_t*>(args.a.out + (int64_t)b * kv.Hq * D);
-    for (int i = tid; i < kv.Hq * D / 2; i += kThreads) o[i] = 0u;
-    if (args.a.lse)
-      for (int i = tid; i < kv.Hq; i += kThreads) args.a.lse[(int64_t)b * kv.Hq + i] = kNegInf;
-  }
-
-  const int total = s_sum[kThreads], warps = (int)gridDim.x * R::kWarps;
-  const int chunk = max(kMinEntries / TILE, (total + warps - 1) / warps);
-  const int j = warp * gridDim.x + blockIdx.x;  // neighbours in the batch sit on different SMs
-  const int lo = (int)min((int64_t)j * chunk, (int64_t)total), hi = min(lo + chunk, total);
-  if (lo >= hi) {
-    if (lane == 0) args.w.chunks[j] = Chunk{-1, 0, 0, 0, 0, chunk, -1, 0, 0, 0, {0, 0}};
-    return;
-  }
-
-  // The place of tile `lo`: the thread share that holds it, then its sequences.
-  Place cons;
-  int row_first;  // first tile of the present row in the batch's order
-  {
+    total = s_sum[kThreads];
+    cut();
     int l = 0, h = kThreads;  // s_sum[l] <= lo < s_sum[h]
     while (h - l > 1) {
       const int m = (l + h) >> 1;
       if (s_sum[m] <= lo) l = m;
       else h = m;
     }
-    int base = s_sum[l];
+    base = s_sum[l];
     cons.b = l * per;
-    for (;; cons.b++) {
+    for (; lo < hi; cons.b++) {
       cons.len = kv_length(kv, cons.b);
-      cons.nt = tiles_of<TILE>(cons.len);
-      if (lo < base + cons.nt * items) break;
-      base += cons.nt * items;
+      const int n = tiles_of<TILE>(cons.len) * items;
+      if (lo < base + n) break;
+      base += n;
     }
-    cons.hh = (lo - base) / cons.nt;
-    cons.t = (lo - base) - cons.hh * cons.nt;
-    row_first = lo - cons.t;
   }
+  // Idle rows, from the last warps on, which have no tiles in a small batch: out 0, lse -inf.
+  auto idle_rows = [&] {
+    for (int b = warps - 1 - j; b < kv.n_seqs; b += warps) {
+      if (kv_length(kv, b) != 0) continue;
+      uint4* o = reinterpret_cast<uint4*>(args.a.out + (int64_t)b * kv.Hq * D);
+      for (int i = lane; i < kv.Hq * D / 8; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (args.a.lse)
+        for (int i = lane; i < kv.Hq; i += 32) args.a.lse[(int64_t)b * kv.Hq + i] = kNegInf;
+    }
+  };
+  if (lo >= hi) {
+    idle_rows();
+    if (lane == 0) args.w.chunks[j] = Chunk{-1, 0, 0, 0, 0, chunk, -1, 0, 0, 0, {0, 0}};
+    return;
+  }
+  cons.nt = tiles_of<TILE>(cons.len);
+  cons.hh = (lo - base) / cons.nt;
+  cons.t = (lo - base) - cons.hh * cons.nt;
+  int row_first = lo - cons.t;  // first tile of the present row in the batch's order
   Chunk left{cons.b, cons.hh, row_first, cons.len, hi - lo, chunk, -1, 0, 0, 0, {0, 0}};
 
   uint8_t* const ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u) + warp * (R::kStages * R::kStage);
@@ -352,15 +402,14 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     __syncwarp();
     if (row >= 0) {
       uint8_t* const at = ring + stage * R::kStage + ((lane << box_shift) * R::kBox);
-#pragma unroll
-      for (int i = 0; i < R::kBoxes; i++) {
-        tc::tma_2d(at + i * R::kBoxBytes, &args.k_map, i * R::kBox, row, full + stage);
-        tc::tma_2d(at + R::kSide + i * R::kBoxBytes, &args.v_map, i * R::kBox, row, full + stage);
+      const int each = (1 << box_shift) == TILE ? R::kBoxes : 1;
+#pragma unroll 1
+      for (int i = 0; i < R::kBoxes; i += each) {
+        tc::tma_3d(at + i * R::kBoxBytes, &args.k_map, 0, row, i, full + stage);
+        tc::tma_3d(at + R::kSide + i * R::kBoxBytes, &args.v_map, 0, row, i, full + stage);
       }
     }
   };
-#pragma unroll 1
-  for (int s = 0; s < R::kStages - 1; s++) load(s);
 
   // ---- consumer ----
   // S^T = K Q^T: 16 entries x 8 heads, O^T = V^T P^T: 16 dims x 8 heads.  A lane
@@ -388,40 +437,17 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
         l[nb][i] = 0.0f;
         qs[nb][i] = unit;
       }
-      if (!E4M3) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks++) {
-          q[ks][nb][0] = real ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + j2) : 0u;
-          q[ks][nb][1] = real ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + j2) : 0u;
-        }
-      } else {
-        // The 16 contraction steps of an mma take the dims 4i, 4i+1 (first half)
-        // and 4i+2, 4i+3 (second half) of each lane i of a quad: the order in which
-        // ldmatrix hands out the bytes of a key.  q joins them as f16 with a
-        // power-of-two factor that puts the head's largest magnitude into
-        // [2^14, 2^15): exact for bf16 values down to 2^-28 of it.
-        float top = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ks++) {
-          const uint2 raw = real ? *reinterpret_cast<const uint2*>(src + ks * 16 + 2 * j2) : make_uint2(0u, 0u);
-          q[ks][nb][0] = raw.x;
-          q[ks][nb][1] = raw.y;
-          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(raw.x)), fabsf(bf16_hi(raw.x))),
-                                 fmaxf(fabsf(bf16_lo(raw.y)), fabsf(bf16_hi(raw.y)))));
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent; 0 and 255: as it is
-        const bool usual = e > 14 && e < 255;
-        const float up = usual ? __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23) : 1.0f;
-        const float down = usual ? unit * __uint_as_float((uint32_t)(e - 14) << 23) : unit;
-#pragma unroll
-        for (int i = 0; i < 2; i++) qs[nb][i] = __shfl_sync(0xffffffffu, down, (j2 + i) * 4);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ks++)
-#pragma unroll
-          for (int i = 0; i < 2; i++)
-            q[ks][nb][i] = f16x2(bf16_lo(q[ks][nb][i]) * up, bf16_hi(q[ks][nb][i]) * up);
+      for (int ks = 0; ks < D / 16; ks++) {
+        // E4M3: the 16 contraction steps of an mma take the dims 4i, 4i+1 (first
+        // half) and 4i+2, 4i+3 (second half) of each lane i of a quad: the order in
+        // which ldmatrix hands out the bytes of a key.
+        const uint2 x = !real ? make_uint2(0u, 0u)
+                        : E4M3 ? *reinterpret_cast<const uint2*>(src + ks * 16 + 2 * j2)
+                               : make_uint2(*reinterpret_cast<const uint32_t*>(src + ks * 16 + j2),
+                                            *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + j2));
+        q[ks][nb][0] = x.x;
+        q[ks][nb][1] = x.y;
       }
     }
 #pragma unroll
@@ -430,6 +456,33 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
       for (int nb = 0; nb < NB; nb++)
 #pragma unroll
         for (int i = 0; i < 4; i++) o[n][nb][i] = 0.0f;
+  };
+
+  // For an E4M3 cache q becomes f16 with a power-of-two factor that puts the head's
+  // largest magnitude into [2^14, 2^15): exact for bf16 values down to 2^-28 of it.
+  auto encode_row = [&] {
+#pragma unroll
+    for (int nb = 0; nb < NB; nb++) {
+      float top = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ks++)
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+          top = fmaxf(top, fmaxf(fabsf(bf16_lo(q[ks][nb][i])), fabsf(bf16_hi(q[ks][nb][i]))));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent; 0 and 255: as it is
+      const bool usual = e > 14 && e < 255;
+      const float up = usual ? __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23) : 1.0f;
+      const float down = usual ? __uint_as_float((uint32_t)(e - 14) << 23) : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 2; i++) qs[nb][i] *= __shfl_sync(0xffffffffu, down, (j2 + i) * 4);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ks++)
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+          q[ks][nb][i] = f16x2(bf16_lo(q[ks][nb][i]) * up, bf16_hi(q[ks][nb][i]) * up);
+    }
   };
 
   // Rows g and g + 8 of the n-th block of O^T are the dims 16n + g and 16n + g + 8
@@ -497,9 +550,12 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
   uint32_t phase = 0;
   bool broken = false;
   bool fresh = true;  // a row begins with this tile
+  begin_row(cons.b, cons.hh);  // q is on its way before the tiles fill the memory's queues
+#pragma unroll 1
+  for (int s = 0; s < R::kStages - 1; s++) load(s);
 #pragma unroll 1
   for (int at = lo; at < hi; at++) {
-    if (fresh) begin_row(cons.b, cons.hh);
+    if (E4M3 && fresh) encode_row();
     {
       const int ahead = stage + R::kStages - 1;
       load(ahead >= R::kStages ? ahead - R::kStages : ahead);
@@ -594,13 +650,14 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
         over |= x > m[nb][i] + kSlack;
       }
     if (MASS && at < args.w.tiles) {
-      float* sc = args.w.scores + (int64_t)at * (8 * NB * TILE) + j2 * TILE + g;
+      float* sc = args.w.scores + ((int64_t)at * TILE + g) * (8 * NB) + j2;
 #pragma unroll
       for (int t = 0; t < NT; t++)
 #pragma unroll
-        for (int nb = 0; nb < NB; nb++)
+        for (int e = 0; e < 2; e++)
 #pragma unroll
-          for (int i = 0; i < 4; i++) sc[(8 * nb + (i & 1)) * TILE + 16 * t + 8 * (i >> 1)] = s[t][nb][i];
+          for (int nb = 0; nb < NB; nb++)
+            *reinterpret_cast<float2*>(sc + (16 * t + 8 * e) * (8 * NB) + 8 * nb) = make_float2(s[t][nb][2 * e], s[t][nb][2 * e + 1]);
     }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -690,7 +747,10 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
         left.go_parts = (row_first + cons.nt - 1) / chunk - left.go_j0 + 1;
       }
       row_first += cons.nt;
-      if (at + 1 < hi) advance<TILE>(kv, cons, items);
+      if (at + 1 < hi) {
+        advance<TILE>(kv, cons, items);
+        begin_row(cons.b, cons.hh);
+      }
       fresh = true;
     } else {
       cons.t++;
@@ -709,6 +769,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     left.go_b = -1;
   }
   if (lane == 0) args.w.chunks[j] = left;
+  idle_rows();
   if (MASS && lane == 0 && hi > args.w.tiles) set_status(kv.status, kStBadId);
 }
 
@@ -718,8 +779,9 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
 // in many parts has many blocks.  Part p lies on chunk j0 + p, side 1 (the row
 // begins) for p = 0, else side 0.
 //
-// With MASS block j then adds the weights of chunk j's entries: 2^(score - lse)
-// over the query heads of their KV head.
+// With MASS it then adds the weights of chunk j's entries: 2^(score - lse)
+// over the query heads of their KV head.  Every warp of both goes its own way: one
+// trip to memory for what it joins.
 // ---------------------------------------------------------------------------
 struct JoinArgs {
   KvAttnArgs a;
@@ -727,123 +789,159 @@ struct JoinArgs {
   int groups;
 };
 
-constexpr int kJoinThreads = 128;   // 8 threads for the statistics of each of 16 rows
+constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
-// m and l of the rows of an item over their parts, by 8 threads a row.
-__device__ __forceinline__ void join_ml(const float2* ml, int j0, int parts, float2* s_ml) {
-  const int row = threadIdx.x >> 3, sub = threadIdx.x & 7;
-  float top = kNegInf, sum = 0.0f;
-  auto add = [&](float2 x) {  // a part without a score: l is 0, or NaN
-    const float both = fmaxf(top, x.x);
-    sum = (top == both ? sum : sum * exp2_fast(top - both)) + (x.x == both || x.x == kNegInf ? x.y : x.y * exp2_fast(x.x - both));
-    top = both;
-  };
-#pragma unroll 4
-  for (int p = sub; p < parts; p += 8) add(ml[((int64_t)(j0 + p) * 2 + (p == 0 ? 1 : 0)) * kRows + row]);
-#pragma unroll
-  for (int d = 4; d > 0; d >>= 1) {
-    const float2 x = make_float2(__shfl_xor_sync(0xffffffffu, top, d), __shfl_xor_sync(0xffffffffu, sum, d));
-    add(x);
+// What a sum with reference x counts for under the reference `both` >= x.
+__device__ __forceinline__ float rescale(float x, float both) { return x == both ? 1.0f : exp2_fast(x - both); }
+
+template <int D>
+__device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
+  const KvView& kv = args.a.kv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = c.go_hh / args.groups, gi = c.go_hh - h * args.groups;
+  const int n_rows = min(kRows, kv.G - gi * kRows);
+  const int64_t head0 = (int64_t)c.go_b * kv.Hq + h * kv.G + gi * kRows;
+  const int parts = c.go_parts, blocks = parts - 1, mine = (int)blockIdx.x - c.go_j0;
+  // Units of four dims of a row.  `split` lanes share a unit's parts while
+  // there are more threads than units.
+  const int units = n_rows * (D / 4), threads = blocks * kJoinThreads;
+  int split = 1;
+  while (split < 32 && split * 2 <= parts && units * split * 2 <= threads) split *= 2;
+  const int width = 32 / split;
+  for (int u0 = (mine * kJoinWarps + warp) * width; u0 < units; u0 += blocks * kJoinWarps * width) {
+    const int u = min(u0 + lane % width, units - 1), row = u / (D / 4), d4 = u - row * (D / 4);
+    float top = kNegInf, sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](float m, float l, float4 x) {
+      const float both = fmaxf(top, m), a = rescale(top, both), b = rescale(m, both);
+      top = both;
+      sum = sum * a + l * b;
+      acc.x = acc.x * a + x.x * b;
+      acc.y = acc.y * a + x.y * b;
+      acc.z = acc.z * a + x.z * b;
+      acc.w = acc.w * a + x.w * b;
+    };
+#pragma unroll 8
+    for (int p = lane / width; p < parts; p += split) {
+      const int64_t at = ((int64_t)(c.go_j0 + p) * 2 + (p == 0 ? 1 : 0)) * kRows + row;
+      const float2 ml = args.w.ml[at];
+      add(ml.x, ml.y, *reinterpret_cast<const float4*>(args.w.o + at * D + d4 * 4));
+    }
+    for (int d = width; d < 32; d <<= 1) {
+      const float m = __shfl_xor_sync(0xffffffffu, top, d), l = __shfl_xor_sync(0xffffffffu, sum, d);
+      const float4 x = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, d), __shfl_xor_sync(0xffffffffu, acc.y, d),
+                                   __shfl_xor_sync(0xffffffffu, acc.z, d), __shfl_xor_sync(0xffffffffu, acc.w, d));
+      add(m, l, x);
+    }
+    if (lane >= width || u0 + lane >= units) continue;
+    const float inv = sum == 0.0f ? 0.0f : kv.v_scale / sum;
+    *reinterpret_cast<uint2*>(args.a.out + (head0 + row) * D + d4 * 4) =
+        make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+    if (d4 == 0 && args.a.lse)
+      args.a.lse[head0 + row] = sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
   }
-  if (sub == 0) s_ml[row] = make_float2(top, sum);
 }
 
-template <int D, int TILE, bool MASS>
-__global__ void __launch_bounds__(kJoinThreads, 8) k_kv_join(JoinArgs args) {
-  __shared__ float2 s_ml[kRows];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// The warp's share of a chunk's tiles.  L lanes hold an entry's 8 NB scores, four
+// query heads each; 32 / L entries go at a time, and after L of them each lane
+// has the sum of one entry.
+template <int TILE, int NB>
+__device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
+  constexpr int L = 2 * NB, E = 32 / L;
   const KvView& kv = args.a.kv;
-  kv_pdl_wait();
-  const Chunk c = args.w.chunks[blockIdx.x];
-  if (blockIdx.y == 0) {
-    if (c.go_b < 0) return;
-    const int h = c.go_hh / args.groups, gi = c.go_hh - h * args.groups;
-    const int n_rows = min(kRows, kv.G - gi * kRows);
-    const int64_t head0 = (int64_t)c.go_b * kv.Hq + h * kv.G + gi * kRows;
-    const int j0 = c.go_j0, parts = c.go_parts, blocks = parts - 1, mine = (int)blockIdx.x - j0;
-    join_ml(args.w.ml, j0, parts, s_ml);  // rows above n_rows: whatever memory held, not used
-    __syncthreads();
-    if (mine == 0 && tid < n_rows && args.a.lse)
-      args.a.lse[head0 + tid] = s_ml[tid].y == 0.0f ? kNegInf : (s_ml[tid].x + log2f(s_ml[tid].y)) * 0.6931471805599453f;
-    // Units of four dims of a row.  `split` lanes share a unit's parts while
-    // there are more threads than units.
-    const int units = n_rows * (D / 4), threads = blocks * kJoinThreads;
-    int split = 1;
-    while (split < 32 && split * 2 <= parts && units * split * 2 <= threads) split *= 2;
-    const int width = 32 / split;
-    for (int u0 = (mine * kJoinWarps + warp) * width; u0 < units; u0 += blocks * kJoinWarps * width) {
-      const int u = min(u0 + lane % width, units - 1), row = u / (D / 4), d4 = u - row * (D / 4);
-      const float2 ml = s_ml[row];
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int p = lane / width; p < parts; p += split) {
-        const int64_t at = ((int64_t)(j0 + p) * 2 + (p == 0 ? 1 : 0)) * kRows + row;
-        const float m = args.w.ml[at].x;
-        const float4 x = *reinterpret_cast<const float4*>(args.w.o + at * D + d4 * 4);
-        const float w = m == kNegInf ? 0.0f : exp2_fast(m - ml.x);
-        acc.x += w * x.x;
-        acc.y += w * x.y;
-        acc.z += w * x.z;
-        acc.w += w * x.w;
-      }
-      for (int d = width; d < 32; d <<= 1) {
-        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, d);
-        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, d);
-        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, d);
-        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, d);
-      }
-      const float inv = ml.y == 0.0f ? 0.0f : kv.v_scale / ml.y;
-      if (lane < width && u0 + lane < units)
-        *reinterpret_cast<uint2*>(args.a.out + (head0 + row) * D + d4 * 4) =
-            make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
-    }
-    return;
-  }
-  if (!MASS || c.tiles == 0) return;
-
-  const int items = kv.Hkv * args.groups, rows_kept = kv.G > 8 ? 16 : 8;
-  const int lo = (int)blockIdx.x * c.size, hi = lo + c.tiles;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L, set = lane / L;
+  const int items = kv.Hkv * args.groups, share = (c.tiles + kJoinWarps - 1) / kJoinWarps;
+  const int chunk0 = (int)blockIdx.x * c.size, lo = chunk0 + min(c.tiles, warp * share), hi = min(chunk0 + c.tiles, lo + share);
   Place p{c.b, c.hh, 0, c.len, tiles_of<TILE>(c.len)};
   for (int first = c.first; first < hi;) {
     const int h = p.hh / args.groups;
-    if (p.hh == h * args.groups) {  // the first group's tiles stand for the entries; all groups are added there
-      const int t0 = max(lo, first) - first, t1 = min(hi, first + p.nt) - first;
-      for (int gi = 0; gi < args.groups; gi++) {
-        const int row_first = first + gi * p.nt, j0 = row_first / c.size;
-        const int parts = (row_first + p.nt - 1) / c.size - j0 + 1, n_rows = min(kRows, kv.G - gi * kRows);
-        __syncthreads();
-        if (parts == 1) {  // written as m = lse, l = 1
-          if (tid < n_rows) s_ml[tid] = make_float2(args.w.lse2[(int64_t)p.b * kv.Hq + h * kv.G + gi * kRows + tid], 1.0f);
-        } else {
-          join_ml(args.w.ml, j0, parts, s_ml);
-        }
-        __syncthreads();
-        if (tid < n_rows) s_ml[tid].x = s_ml[tid].y == 0.0f ? kNegInf : s_ml[tid].x + log2f(s_ml[tid].y);
-        __syncthreads();
-        // four entries a thread
-        for (int e = t0 * TILE + tid * 4; e < min(t1 * TILE, p.len); e += kJoinThreads * 4) {
-          const int64_t tile = row_first + e / TILE;
-          if (tile >= args.w.tiles) break;
-          const float* sc = args.w.scores + tile * rows_kept * TILE + e % TILE;
-          float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-          for (int r = 0; r < n_rows; r++) {
-            const float z = s_ml[r].x;
-            const float4 x = *reinterpret_cast<const float4*>(sc + r * TILE);
-            if (z == kNegInf) continue;  // no weight anywhere
-            sum.x += exp2_fast(x.x - z);
-            sum.y += exp2_fast(x.y - z);
-            sum.z += exp2_fast(x.z - z);
-            sum.w += exp2_fast(x.w - z);
+    // the first group's tiles stand for the entries; all groups are added there
+    const bool counts = p.hh == h * args.groups && first + p.nt > lo;
+    const int e0 = (max(lo, first) - first) * TILE, e1 = min((min(hi, first + p.nt) - first) * TILE, p.len);
+    for (int gi = 0; counts && gi < args.groups; gi++) {
+      const int row_first = first + gi * p.nt, j0 = row_first / c.size;
+      const int parts = (row_first + p.nt - 1) / c.size - j0 + 1, n_rows = min(kRows, kv.G - gi * kRows);
+      const float* const scores = args.w.scores + (int64_t)row_first * TILE * (8 * NB) + sub * 4;
+      const int last = (int)min((int64_t)e1, (args.w.tiles - row_first) * TILE);  // entries whose scores were kept
+      float4 x[2][L];
+      int row[2];
+      auto load = [&](int e) {  // two runs of 32 entries; the lane keeps the sum of entry sub * E + set of each
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+          const int own = e + 32 * r + sub * E + set;
+          row[r] = own < last ? kv_row(kv, p.b, h, own) : -1;
+#pragma unroll
+          for (int k = 0; k < L; k++) {
+            const int at = e + 32 * r + k * E + set;
+            x[r][k] = at < last ? *reinterpret_cast<const float4*>(scores + (int64_t)at * (8 * NB))
+                                : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
           }
-          const float add[4] = {sum.x, sum.y, sum.z, sum.w};
+        }
+      };
+      if (e0 < last) load(e0);
+      float z[4];  // lse of the lane's heads; +inf takes a head (without weights, or none) out
+      if (parts == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          z[i] = sub * 4 + i < n_rows ? args.w.lse2[(int64_t)p.b * kv.Hq + h * kv.G + gi * kRows + sub * 4 + i] : kNegInf;
+      } else {
+        auto part = [&](int q, float (&m)[4], float (&l)[4]) {
+          const float4* ml = reinterpret_cast<const float4*>(args.w.ml + ((int64_t)(j0 + q) * 2 + (q == 0 ? 1 : 0)) * kRows + sub * 4);
+          const float4 u = ml[0], v = ml[1];
+          m[0] = u.x, l[0] = u.y, m[1] = u.z, l[1] = u.w, m[2] = v.x, l[2] = v.y, m[3] = v.z, l[3] = v.w;
+        };
+        float top[4], sum[4] = {}, m[4], l[4];
+        part(min(set, parts - 1), m, l);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          top[i] = m[i];
+          if (set >= parts) l[i] = 0.0f;
+        }
+        for (int q = set + E; q < parts; q += E) {
+          float mq[4], lq[4];
+          part(q, mq, lq);
 #pragma unroll
           for (int i = 0; i < 4; i++) {
-            const int row = e + i < p.len ? kv_row(kv, p.b, h, e + i) : -1;
-            if (row >= 0) kv.mass[row] += add[i];
+            const float both = fmaxf(top[i], mq[i]);
+            l[i] = l[i] * rescale(top[i], both) + lq[i] * rescale(mq[i], both);
+            top[i] = both;
           }
         }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          m[i] = top[i];
+#pragma unroll
+          for (int d = L; d < 32; d <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], d));
+          sum[i] = l[i] * rescale(m[i], top[i]);
+#pragma unroll
+          for (int d = L; d < 32; d <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
+          z[i] = sub * 4 + i < n_rows && sum[i] != 0.0f ? top[i] + __log2f(sum[i]) : kNegInf;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (z[i] == kNegInf) z[i] = -kNegInf;
+#pragma unroll 1
+      for (int e = e0; e < last;) {
+        float old[2];
+#pragma unroll
+        for (int r = 0; r < 2; r++) old[r] = row[r] >= 0 ? kv.mass[row[r]] : 0.0f;
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+          float mine = 0.0f;
+#pragma unroll
+          for (int k = 0; k < L; k++) {
+            const float4 y = x[r][k];
+            float sum = (exp2_fast(y.x - z[0]) + exp2_fast(y.y - z[1])) + (exp2_fast(y.z - z[2]) + exp2_fast(y.w - z[3]));
+#pragma unroll
+            for (int d = 1; d < L; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (sub == k) mine = sum;
+          }
+          if (row[r] >= 0) kv.mass[row[r]] = old[r] + mine;
+        }
+        e += 64;
+        if (e < last) load(e);
       }
     }
     first += p.nt;
@@ -852,6 +950,15 @@ __global__ void __launch_bounds__(kJoinThreads, 8) k_kv_join(JoinArgs args) {
       advance<TILE>(kv, p, items);
     }
   }
+}
+
+template <int D, int TILE, int NB, bool MASS>
+__global__ void __launch_bounds__(kJoinThreads, 8) k_kv_join(JoinArgs args) {
+  kv_pdl_trigger();
+  kv_pdl_wait();
+  const Chunk c = args.w.chunks[blockIdx.x];
+  if (c.go_b >= 0) join_row<D>(args, c);
+  if (MASS && c.tiles > 0) add_mass<TILE, NB>(args, c);
 }
 
 template <int D, bool E4M3, int NB, bool MASS>
@@ -863,20 +970,17 @@ cudaError_t run(SplitArgs& a, int sms, cudaStream_t s) {
   const uint64_t rows = (uint64_t)kv.n_pages * kv.Hkv << kv.page_shift;
   a.box_shift = R::kTile == 32 ? 5 : 4;
   if (kv.page_shift < a.box_shift) a.box_shift = kv.page_shift;
-  if (encode_tmap_rows(&a.k_map, kv.k, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift) != FT_OK ||
-      encode_tmap_rows(&a.v_map, kv.v, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift) != FT_OK)
+  a.per_warp = 1.0f / (float)(sms * R::kWarps);
+  const uint32_t deep = (1 << a.box_shift) == R::kTile ? R::kBoxes : 1;
+  if (encode_tmap_rows(&a.k_map, kv.k, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift, deep) != FT_OK ||
+      encode_tmap_rows(&a.v_map, kv.v, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift, deep) != FT_OK)
     return cudaErrorInvalidValue;
   auto kern = k_kv_split<D, E4M3, NB, MASS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
   if (e != cudaSuccess) return e;
-  kern<<<sms, R::kWarps * 32, R::kBytes, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = kv_launch_after(kern, dim3((unsigned)sms), R::kWarps * 32, R::kBytes, s, a)) != cudaSuccess) return e;
   const JoinArgs ja{a.a, a.w, a.groups};
-  // The same split of the SMs' memory as the kernel before it: no SM has to change over between the two.
-  auto join = k_kv_join<D, R::kTile, MASS>;
-  e = cudaFuncSetAttribute(join, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-  if (e != cudaSuccess) return e;
-  return kv_launch_after(join, dim3((unsigned)(sms * R::kWarps), MASS ? 2 : 1), kJoinThreads, 0, s, ja);
+  return kv_launch_after(k_kv_join<D, R::kTile, NB, MASS>, dim3((unsigned)(sms * R::kWarps)), kJoinThreads, 0, s, ja);
 }
 
 template <int D, bool E4M3>

@@ -563,7 +563,8 @@ typedef struct {
   int32_t n_kv_heads;
   int32_t page_size;     /* entries of a page: a power of two from 8 to 1024 */
   int32_t n_seqs;        /* rows of block_table and lengths, at most 65536 (0: every call is a no-op) */
-  int32_t max_pages;     /* columns of block_table; max_pages * page_size <= 2^30 */
+  int32_t max_pages;     /* columns of block_table; max_pages * page_size <= 2^30, and n_seqs * n_kv_heads
+                            times its 16ths (and times the 16ths of n_heads/n_kv_heads) below 2^30 */
   int64_t n_pages;       /* pages of the pools; n_pages * n_kv_heads * page_size < 2^31 */
   int32_t format;        /* FT_KV_BF16 or FT_KV_E4M3 */
   float k_scale;         /* what one unit of a stored key / value stands for (E4M3: positive and finite; */
