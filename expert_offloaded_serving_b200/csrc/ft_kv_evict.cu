@@ -85,7 +85,7 @@ __device__ __forceinline__ uint32_t warps_before(uint32_t mine, uint32_t* s, uin
 // N: entries of a thread that are in registers.  ONE: that is all of them (a block's
 // share of the longest possible sequence); else every pass reads them again in rounds.
 template <int N, bool ONE>
-__global__ void __launch_bounds__(kSelThreads, N <= 16 ? 2 : 1) k_kv_select(SelectArgs args) {
+__global__ void __launch_bounds__(kSelThreads, ONE && N <= 16 ? 2 : 1) k_kv_select(SelectArgs args) {
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ SelectShared sh;
   const KvView& kv = args.a.kv;
@@ -135,11 +135,10 @@ __global__ void __launch_bounds__(kSelThreads, N <= 16 ? 2 : 1) k_kv_select(Sele
   const int w_begin = min(end, begin + warp * warp_share), w_end = min(end, w_begin + warp_share);
   const int32_t* const pages = kv.table + (int64_t)b * kv.max_pages;
 
-  // Entry i0 + 32 e + lane, for e < N: position (-1: none) and mass key.
-  int pos[N];
+  // Entry i0 + 32 e + lane, for e < N: row (-1: none), position (-1: none), mass key.
+  int row[N], pos[N];
   uint32_t key[N];
   auto load = [&](int i0) {
-    int row[N];
 #pragma unroll
     for (int e = 0; e < N; e++) {
       const int i = i0 + 32 * e + lane;
@@ -152,12 +151,11 @@ __global__ void __launch_bounds__(kSelThreads, N <= 16 ? 2 : 1) k_kv_select(Sele
       if (i < w_end && !real) set_status(kv.status, kStBadId);
       row[e] = real ? ((row[e] * kv.Hkv + h) << kv.page_shift) + (i & kv.page_mask) : -1;
       pos[e] = real ? kv.pos[row[e]] : -1;
+      key[e] = real ? __float_as_uint(kv.mass[row[e]]) : 0u;  // no page: nothing there to keep
     }
 #pragma unroll
-    for (int e = 0; e < N; e++) {
-      const float m = row[e] >= 0 ? kv.mass[row[e]] : 0.0f;  // no page: nothing there to keep
-      key[e] = m > 0.0f ? __float_as_uint(m) : 0u;
-    }
+    for (int e = 0; e < N; e++)
+      if (!(__uint_as_float(key[e]) > 0.0f)) key[e] = 0u;
   };
   int recent_above = 0;  // positions above this one are recent
   auto rank_recent = [&] {
@@ -187,7 +185,7 @@ __global__ void __launch_bounds__(kSelThreads, N <= 16 ? 2 : 1) k_kv_select(Sele
   if (ONE && w_begin >= w_end) {
 #pragma unroll
     for (int e = 0; e < N; e++) {
-      pos[e] = -1;
+      row[e] = pos[e] = -1;
       key[e] = 0u;
     }
   }
@@ -278,7 +276,7 @@ __global__ void __launch_bounds__(kSelThreads, N <= 16 ? 2 : 1) k_kv_select(Sele
     tie += warps_before(mine, sh.warp_sum, all);
   }
   const uint32_t below = (1u << lane) - 1u;
-  // f(slot, is a freed slot, is a survivor to move) for every 32 entries
+  // f(slot, row, is a freed slot, is a survivor to move) for every 32 entries
   auto classify = [&](auto&& f) {
     uint32_t at = tie;
     rounds([&](int i0) {
@@ -293,12 +291,12 @@ __global__ void __launch_bounds__(kSelThreads, N <= 16 ? 2 : 1) k_kv_select(Sele
           if (mine) kept = at + __popc(equal & below) < want;
           at += __popc(equal);
         }
-        f(i, in && !kept && i < budget, kept && i >= budget);
+        f(i, row[e], in && !kept && i < budget, kept && i >= budget);
       }
     });
   };
   uint32_t holes = 0, movers = 0, all_holes, all_movers;
-  classify([&](int, bool is_hole, bool is_mover) {
+  classify([&](int, int, bool is_hole, bool is_mover) {
     holes += is_hole;
     movers += is_mover;
   });
@@ -338,10 +336,10 @@ __global__ void __launch_bounds__(kSelThreads, N <= 16 ? 2 : 1) k_kv_select(Sele
   if (fits) {
     int32_t* const freed = args.w.list + list0;
     int32_t* const from = freed + (len >> 1);
-    classify([&](int i, bool is_hole, bool is_mover) {
+    classify([&](int, int at_row, bool is_hole, bool is_mover) {
       const uint32_t hb = __ballot_sync(0xffffffffu, is_hole), mb = __ballot_sync(0xffffffffu, is_mover);
-      if (is_hole) freed[hole + __popc(hb & below)] = kv_row(kv, b, h, i);
-      if (is_mover) from[mover + __popc(mb & below)] = kv_row(kv, b, h, i);
+      if (is_hole) freed[hole + __popc(hb & below)] = at_row;
+      if (is_mover) from[mover + __popc(mb & below)] = at_row;
       hole += __popc(hb);
       mover += __popc(mb);
     });
@@ -496,7 +494,7 @@ cudaError_t launch_kv_evict(const KvEvictArgs& args, int row_bytes, int sms, cud
                   : each <= 32 ? select<32, true>(a, blocks, s)
                                : select<16, false>(a, blocks, s);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(sms * 8));
+  const dim3 grid((unsigned)(sms * 4));  // all resident: 64 registers a thread
   switch (row_bytes) {
     case 64: return kv_launch_after(k_kv_move<64>, grid, kMoveThreads, 0, s, a);
     case 96: return kv_launch_after(k_kv_move<96>, grid, kMoveThreads, 0, s, a);

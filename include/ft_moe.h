@@ -579,7 +579,7 @@ typedef struct {
 } ft_kv_cache;
 
 #define FT_KV_BF16 0
-#define FT_KV_E4M3 1        /* stored = E4M3(value / scale), nearest even, saturating at 448 */
+#define FT_KV_E4M3 1        /* stored = E4M3(value * (1 / scale)), nearest even, saturating at 448 */
 
 #define FT_KV_MASS 1u       /* ft_kv_attention: add every entry's weight to mass */
 #define FT_ROPE_ADJACENT 1u /* ft_kv_append: pairs (2i, 2i+1) instead of (i, i + rot_dim/2) */
