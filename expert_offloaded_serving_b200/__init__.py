@@ -71,16 +71,12 @@ class CacheStats(C.Structure):
 
 
 class KvCache(C.Structure):
-    """ft_kv_cache: a layer's paged key-value cache (see make_kv)."""
+    """ft_kv_cache: a layer's paged key-value cache (made by make_kv)."""
     _fields_ = [("head_dim", C.c_int32), ("n_heads", C.c_int32), ("n_kv_heads", C.c_int32), ("page_size", C.c_int32),
                 ("n_seqs", C.c_int32), ("max_pages", C.c_int32), ("n_pages", C.c_int64), ("format", C.c_int32),
                 ("k_scale", C.c_float), ("v_scale", C.c_float), ("k", C.c_void_p), ("v", C.c_void_p),
                 ("mass", C.c_void_p), ("pos", C.c_void_p), ("block_table", C.c_void_p), ("lengths", C.c_void_p),
                 ("status", C.c_void_p)]
-
-    @property
-    def ref(self):
-        return C.byref(self)
 
 
 _lib = None
@@ -176,10 +172,19 @@ def _ptr(t, size: int | None = None) -> int | None:
     return t.data_ptr()
 
 
+_current = None  # torch's current device and raw current stream of a device, once a call needed them
+
+
 def _stream(s) -> int | None:
+    global _current
     if s is None:
-        import torch
-        return torch.cuda.current_stream(torch.cuda.current_device()).cuda_stream
+        if _current is None:
+            import torch
+            # a Stream object takes a microsecond and more to make, where torch hands out the bare handle
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            _current = (torch.cuda.current_device, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+        device, stream = _current
+        return stream(device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -431,6 +436,8 @@ def make_kv(n_heads, k, v, block_table, lengths, mass=None, pos=None, k_scale=1.
                  FT_KV_BF16 if kind == "bfloat16" else FT_KV_E4M3, k_scale, v_scale, _ptr(k, es), _ptr(v, es),
                  _ptr(mass, 4), _ptr(pos, 4), _ptr(block_table, 4), _ptr(lengths, 4), _ptr(status, 4))
     kv.tensors = (k, v, mass, pos, block_table, lengths, status)
+    kv.dims = (d, n_heads, n_kv, block_table.shape[0])
+    kv.ref = C.byref(kv)
     return kv
 
 
@@ -443,11 +450,11 @@ def _dev(t, size: int) -> int | None:
     return _ptr(t, size)
 
 
-def _rows(t, name, heads, d) -> tuple[int, int]:
+def _rows(t, name, rows, heads, d) -> tuple[int, int]:
     """Address and row stride (elements) of q, k or v [rows][heads][d]; rows may be apart, a row is dense."""
-    shape, (row, head, one) = t.shape, t.stride()
-    if shape[1] != heads or shape[2] != d or t.element_size() != 2:
-        raise ValueError(f"{name} {tuple(shape)} {t.dtype}: bf16 [rows][{heads}][{d}]")
+    if t.shape != (rows, heads, d) or t.element_size() != 2:
+        raise ValueError(f"{name} {tuple(t.shape)} {t.dtype}: bf16 [{rows}][{heads}][{d}]")
+    row, head, one = t.stride()
     if one != 1 or (head != d and heads > 1):
         raise ValueError(f"{name} of strides {t.stride()}: the heads of a row are dense")
     return t.data_ptr(), row
@@ -463,45 +470,53 @@ def ft_kv_append(kv: KvCache, q, k, v, cu_new, positions, inv_freq, axis, q_out,
     """q [T][n_heads][D] and q_out (or None, both), k and v [T][n_kv_heads][D] (rows may be apart), cu_new int32
     [n_seqs+1] or None, positions int32 [axes][T], inv_freq float64 and axis int32 [rot_dim/2] (or None, both: no
     rotation)."""
-    d, hk, hq = kv.head_dim, kv.n_kv_heads, kv.n_heads
+    d, hq, hk, n_seqs = kv.dims
     T = k.shape[0]
-    kp, ks = _rows(k, "k", hk, d)
-    vp, vs = _rows(v, "v", hk, d)
-    qp, qs = _rows(q, "q", hq, d) if q is not None else (None, 0)
-    if v.shape[0] != T or (q is not None and q.shape[0] != T):
-        raise ValueError(f"q, k and v of different rows: {None if q is None else q.shape[0]}, {T}, {v.shape[0]}")
+    kp, ks = _rows(k, "k", T, hk, d)
+    vp, vs = _rows(v, "v", T, hk, d)
+    qp, qs = _rows(q, "q", T, hq, d) if q is not None else (None, 0)
     if q_out is not None and q_out.shape != (T, hq, d):
         raise ValueError(f"q_out of shape {tuple(q_out.shape)}: {(T, hq, d)}")
-    if cu_new is not None and cu_new.shape != (kv.n_seqs + 1,):
-        raise ValueError(f"cu_new of shape {tuple(cu_new.shape)}: {(kv.n_seqs + 1,)}")
-    if positions is not None and (positions.dim() != 2 or positions.shape[1] != T):
-        raise ValueError(f"positions of shape {tuple(positions.shape)}: [axes][{T}]")
+    if cu_new is not None and cu_new.shape != (n_seqs + 1,):
+        raise ValueError(f"cu_new of shape {tuple(cu_new.shape)}: {(n_seqs + 1,)}")
+    axes = 0
+    if positions is not None:
+        if positions.dim() != 2 or positions.shape[1] != T:
+            raise ValueError(f"positions of shape {tuple(positions.shape)}: [axes][{T}]")
+        axes = positions.shape[0]
     half = 0 if inv_freq is None else inv_freq.shape[0]
     if (inv_freq is None) != (axis is None) or (axis is not None and axis.shape != (half,)):
         raise ValueError("inv_freq and axis: [rot_dim/2] each, or None")
-    _check(lib().ft_kv_append(kv.ref, T, qp, qs, kp, ks, vp, vs, _dev(cu_new, 4), _dev(positions, 4),
-                              0 if positions is None else positions.shape[0], _dev(inv_freq, 8), _dev(axis, 4),
-                              2 * half, _dev(q_out, 2), flags, _stream(stream)))
+    st = lib().ft_kv_append(kv.ref, T, qp, qs, kp, ks, vp, vs, _dev(cu_new, 4), _dev(positions, 4), axes,
+                            _dev(inv_freq, 8), _dev(axis, 4), 2 * half, _dev(q_out, 2), flags, _stream(stream))
+    if st:
+        _check(st)
 
 
 def ft_kv_attention(kv: KvCache, q, scale, out, lse, workspace, flags=0, stream=None) -> None:
     """q [n_seqs][n_heads][D] (rows may be apart), out dense of that shape, lse float32 [n_seqs][n_heads] or None,
     workspace uint8."""
-    qp, qs = _rows(q, "q", kv.n_heads, kv.head_dim)
-    if q.shape[0] != kv.n_seqs or out.shape != q.shape:
-        raise ValueError(f"q {tuple(q.shape)} and out {tuple(out.shape)}: {kv.n_seqs} rows each")
-    if lse is not None and lse.shape != (kv.n_seqs, kv.n_heads):
-        raise ValueError(f"lse of shape {tuple(lse.shape)}: {(kv.n_seqs, kv.n_heads)}")
-    _check(lib().ft_kv_attention(kv.ref, qp, qs, scale, _dev(out, 2), _dev(lse, 4), _dev(workspace, 1),
-                                 workspace.numel(), flags, _stream(stream)))
+    d, hq, _, n_seqs = kv.dims
+    qp, qs = _rows(q, "q", n_seqs, hq, d)
+    if out.shape != (n_seqs, hq, d):
+        raise ValueError(f"out of shape {tuple(out.shape)}: {(n_seqs, hq, d)}")
+    if lse is not None and lse.shape != (n_seqs, hq):
+        raise ValueError(f"lse of shape {tuple(lse.shape)}: {(n_seqs, hq)}")
+    st = lib().ft_kv_attention(kv.ref, qp, qs, scale, _dev(out, 2), _dev(lse, 4), _dev(workspace, 1), workspace.numel(),
+                               flags, _stream(stream))
+    if st:
+        _check(st)
 
 
 def ft_kv_evict(kv: KvCache, budgets, recent, workspace, stream=None) -> None:
     """budgets int32 [n_seqs], workspace uint8."""
-    if budgets.shape != (kv.n_seqs,):
-        raise ValueError(f"budgets of shape {tuple(budgets.shape)}: {(kv.n_seqs,)}")
-    _check(lib().ft_kv_evict(kv.ref, _dev(budgets, 4), recent, _dev(workspace, 1), workspace.numel(), _stream(stream)))
+    n_seqs = kv.dims[3]
+    if budgets.shape != (n_seqs,):
+        raise ValueError(f"budgets of shape {tuple(budgets.shape)}: {(n_seqs,)}")
+    st = lib().ft_kv_evict(kv.ref, _dev(budgets, 4), recent, _dev(workspace, 1), workspace.numel(), _stream(stream))
+    if st:
+        _check(st)
 
 
 def ft_kv_sync_status(kv: KvCache, stream=None) -> None:
-    _check(lib().ft_kv_sync_status(kv.ref, _stream(stream)))
+    _check(lib().ft_kv_sync_status(C.byref(kv), _stream(stream)))
