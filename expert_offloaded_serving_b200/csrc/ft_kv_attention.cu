@@ -7,28 +7,33 @@
 //   O' = O 2^(m - m') + p V;  at the end out = O / l, lse = ln 2 (m + log2 l).
 // Two parts of one row join the same way: weights 2^(m_i - max m).
 //
-// What bounds it: every cached byte is read once and meets G query heads,
-// 4 G flops for 4 bytes of a BF16 entry.  At the measured copy rate an SM gets
-// 22 bytes a clock, so 16 heads are 90 multiply-adds a clock an SM: far below what
-// mma.sync does, a multiple of what the fp32 pipe could do next to the softmax.
-// So the products run on mma.sync with the heads of one KV head as the 16
-// rows of the tile (idle rows cost nothing that is short), and everything
-// else serves the stream of loads.
+// What bounds it: every cached byte is read once and meets G query heads, 4 G flops
+// for 4 bytes of a BF16 entry.  At the measured copy rate an SM gets 22 bytes a
+// clock, so 16 heads are 90 multiply-adds a clock an SM: far below what mma.sync
+// does, a multiple of what the fp32 pipe could do next to the softmax.  So the
+// products run on mma.sync, the entries as the 16 rows of a tile and 8 or 16 query
+// heads of one KV head as its columns, and everything else serves the stream of
+// loads: a tile of keys or values is one TMA copy into the ring of the warp that
+// uses it.
 //
-// Split: the unit is a tile of 16 entries of one (sequence, KV head, group of
-// 16 query heads).  All tiles of the batch, in that order, are cut into
-// equal contiguous chunks, one a warp; a warp streams its chunk through its own
-// ring of cp.async stages in shared memory and meets no barrier with other
-// warps.  A row (the tiles of one item) that lies inside one chunk is
-// finished there; the parts of the others go to the workspace (fp32) and
-// k_kv_join adds them in the order of the chunks.  Lengths are read on the
-// device: ragged batches and idle rows are balanced by construction, a
-// captured graph stays valid when lengths grow, and the split depends on
-// nothing but the lengths and the number of SMs.
+// Split: the unit is a tile of 16 or 32 entries of one (sequence, KV head, group of
+// 16 query heads).  All tiles of the batch, in that order, are cut into equal
+// contiguous chunks, one a warp; a warp streams its chunk through its own ring and
+// meets no barrier with other warps.  A row (the tiles of one item) that lies inside one
+// chunk is finished there; the parts of the others go to the workspace (fp32) and
+// k_kv_join adds them in the order of the chunks.  Lengths are read on the device:
+// ragged batches and idle rows are balanced by construction, a captured graph stays
+// valid when lengths grow, and the split depends on nothing but the lengths and the
+// number of SMs.
 //
-// With FT_KV_MASS the scores go to the workspace as they come (G fp32 values
-// an entry, next to 4 D bytes of it), and k_kv_mass turns them into weights
-// once the row's lse is known.
+// With FT_KV_MASS the scores go to the workspace as they come (8 or 16 fp32 values an entry,
+// next to its 4 D or 2 D bytes), and k_kv_join turns them into weights once the row's lse
+// is known.
+//
+// Measured (one B200, a graph of passes): 1 x 131,071 entries, 64 query and 8 KV heads of 128, BF16
+// 93 us (5.8 TB/s; the slowest SMs end at 86, the mean one at 77: the share of the
+// memory's rate that an SM gets differs by 13 %); 64 sequences of 300 to 16,000 entries
+// 160 us (6.2 TB/s); 37 entries 7.5 us, two launches and four trips to memory.
 #include "ft_gemm.h"
 #include "ft_kv.cuh"
 #include "ft_tc.cuh"
@@ -38,33 +43,34 @@ namespace ft {
 namespace {
 
 constexpr int kRows = 16;        // query heads of an item: rows of the mma tile
-constexpr int kMaxWarps = 16;     // warps of a block at most
+constexpr int kMaxWarps = 8;      // warps of a block at most
 constexpr int kMaxChunks = kKvMaxSms * kMaxWarps;
 
 // The ring of a warp for entries of RB bytes a side: a stage holds a tile of keys
 // and one of values as TMA leaves them, boxes of kBox bytes x the tile's rows whose
 // 16-byte pieces are swizzled (ldmatrix then reads 8 rows from 8 different
 // groups of banks).
-#ifndef TUNE_TILE
-#define TUNE_TILE(RB) (RB <= 256 ? 32 : 16)
-#define TUNE_WARPS(RB) (RB == 256 ? 6 : RB >= 384 ? 4 : 8)
-#define TUNE_MIN 32
-#endif
+//
+// Tile and warps by what was measured: 32 entries halve the instructions around the
+// products, up to rows of 256 bytes (131,072 entries of 256 bytes 93 us, 16 entries a tile 96).
+// There 4 warps x 3 stages match 6 x 2 on long rows (93 and 92 us) and win on 64 sequences of 200
+// entries (12.4 against 15.3); rows of 128 bytes want 8 warps (a ragged batch 56.8 us, 59.7 with
+// 6); beyond 256 the registers of O leave room for 4.
 template <int RB>
 struct Ring {
-  static constexpr int kTile = TUNE_TILE(RB);  // entries
+  static constexpr int kTile = RB <= 256 ? 32 : 16;  // entries
   static constexpr int kBox = RB % 128 == 0 ? 128 : RB % 64 == 0 ? 64 : 32;
   static constexpr int kBoxes = RB / kBox;
   static constexpr int kBoxBytes = kTile * kBox;
   static constexpr int kSide = kTile * RB;
   static constexpr int kStage = 2 * kSide;
-  static constexpr int kWarps = TUNE_WARPS(RB);
+  static constexpr int kWarps = RB >= 256 ? 4 : 8;
   static constexpr int kFit = 220 * 1024 / (kWarps * kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kBytes = kWarps * kStages * kStage + 1024;  // the swizzle goes by address: aligned to its period
 };
 
-constexpr int tile_of(int row_bytes) { return TUNE_TILE(row_bytes); }
+constexpr int tile_of(int row_bytes) { return row_bytes <= 256 ? 32 : 16; }
 
 // What chunk j leaves for block j of k_kv_join.
 struct __align__(16) Chunk {
@@ -112,6 +118,7 @@ struct SplitArgs {
   AttnWork w;
   int groups;     // items of a KV head: groups of 16 query heads
   float per_warp;  // 1 / warps of the launch
+  float per_part;  // 1 / (rows x kMaxParts)
   int box_shift;  // box_rows = 1 << box_shift: a tile's rows, or a page's where pages are smaller
 };
 
@@ -224,9 +231,11 @@ __device__ __forceinline__ void advance(const KvView& kv, Place& p, int items) {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
-// Tiles a warp takes at least: a row of few entries is read by few warps, whose
-// parts need no (or a short) join.
-constexpr int kMinEntries = TUNE_MIN;
+// Parts a row of mean length is cut into while a warp has fewer than 4 tiles: a warp for
+// every tile of a short row is quickest (each further tile of a warp costs what the
+// join of one more part does not), but one row's hundreds of parts are not (4,000
+// entries, two KV heads of 256: 250 parts 17.3 us, 84 parts 12.7).
+constexpr int kMaxParts = 64;
 
 // A running maximum is replaced once a score passes it by this much (a factor of
 // 256): any reference would do for the sums, and most tiles then need neither
@@ -271,7 +280,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     n += n * warps < total;
     n += n * warps < total;
     n -= (n - 1) * warps >= total && n > 0;
-    return max(kMinEntries / TILE, n);
+    return max(max(n, 1), min(4, (int)((float)total * args.per_part)));
   };
   // The tiles of the batch are counted, cut, and the chunk's first one is looked up: its
   // sequence, and that one's first tile in the batch.
@@ -647,7 +656,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
             x = fmaxf(x, s[t][nb][2 * e + i]);
           }
         top[nb][i] = x;
-        over |= x > m[nb][i] + kSlack;
+        over |= x - m[nb][i] > kSlack;  // the difference is exact where the two are near
       }
     if (MASS && at < args.w.tiles) {
       float* sc = args.w.scores + ((int64_t)at * TILE + g) * (8 * NB) + j2;
@@ -971,6 +980,7 @@ cudaError_t run(SplitArgs& a, int sms, cudaStream_t s) {
   a.box_shift = R::kTile == 32 ? 5 : 4;
   if (kv.page_shift < a.box_shift) a.box_shift = kv.page_shift;
   a.per_warp = 1.0f / (float)(sms * R::kWarps);
+  a.per_part = 1.0f / ((float)kv.n_seqs * (float)(kv.Hkv * a.groups) * kMaxParts);
   const uint32_t deep = (1 << a.box_shift) == R::kTile ? R::kBoxes : 1;
   if (encode_tmap_rows(&a.k_map, kv.k, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift, deep) != FT_OK ||
       encode_tmap_rows(&a.v_map, kv.v, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift, deep) != FT_OK)

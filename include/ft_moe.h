@@ -551,7 +551,9 @@ FT_API ft_status ft_moe_layer_forward_noalloc(int32_t hidden, int32_t inter, int
  * Pages: sequences may share a page that is only read (a common prefix).  A
  * page that a call writes (ft_kv_append's new slots; every page, with
  * FT_KV_MASS or ft_kv_evict) belongs to one sequence and stands once in the
- * table; otherwise the order of the writes to it is open.
+ * table; otherwise the order of the writes to it is open.  The caller orders calls
+ * (and its own writes) on one cache: calls that only read it (ft_kv_attention without
+ * FT_KV_MASS, each with its workspace) may run at the same time.
  *
  * Bad contents that only the device can see (a page outside [0, n_pages), a
  * length that is negative or above max_pages * page_size, an axis or position
@@ -588,7 +590,8 @@ typedef struct {
  * cache (one size covers both).  The workspace needs no initial contents and
  * keeps none from one call for the next; calls that share one must be ordered
  * on the GPU, so two graphs that may run at the same time take two.  Reads
- * the shape only.  FT_ERR_INVALID on a bad shape. */
+ * the shape, and whether mass and pos are there (room for FT_KV_MASS and
+ * ft_kv_evict).  FT_ERR_INVALID on a bad shape. */
 FT_API ft_status ft_kv_workspace_bytes(const ft_kv_cache* kv, int64_t* bytes);
 
 /* Rotate the new tokens' queries and keys by their positions and write keys

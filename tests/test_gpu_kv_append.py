@@ -133,6 +133,41 @@ def test_blocks_of_several_tokens(T):
     assert c.status.item() == 0
 
 
+def test_thousands_of_sequences():
+    """Decode rows and ragged prompts of 3,001 sequences, most of them without new tokens."""
+    lengths = [(i * 31) % 7 for i in range(3001)]
+    c = Cache(lengths, 2, 1, 64, 8, seed=31)
+    step = Step(c, [1 if n else 0 for n in lengths], decode=True)
+    step.run()
+    live = [(i, n) for i, n in enumerate(lengths) if n]
+    rows = torch.tensor([i for i, _ in live], device="cuda")
+    last = torch.tensor([n - 1 for _, n in live], device="cuda")
+    page = c.table.long()[rows, last // 8]
+    assert torch.equal(c.v[page, 0, last % 8], step.v[rows, 0])
+    assert torch.equal(c.pos[page, 0, last % 8], step.positions[0, rows])
+    assert (step.q_out[torch.tensor([i for i, n in enumerate(lengths) if not n], device="cuda")] == 7).all()
+    new = [n if i % 97 == 5 else 0 for i, n in enumerate(lengths)]
+    step = Step(c, new, 2, pad=11, seed=5)
+    step.run()
+    assert c.status.item() == 0
+    for t, b, slot in step.slots():
+        p = int(c.table[b, slot // 8])
+        assert torch.equal(c.v[p, 0, slot % 8], step.v[t, 0]) and int(c.pos[p, 0, slot % 8]) == int(step.positions[0, t])
+    assert (step.q_out[sum(new):] == 7).all() and (step.q_out[:sum(new)] != 7).any()
+
+
+def test_weights_without_positions_and_no_rotation():
+    c = Cache([20, 0, 7], 4, 2, 96, 16, seed=32)
+    c.pos = None
+    step = Step(c, [3, 0, 2], rot=0)
+    step.positions = None
+    k = step.k.clone()
+    step.run()
+    at = c.place(0, torch.arange(17, 20, device="cuda"))
+    assert (c.mass[at] == 0).all() and torch.equal(c.k[at], k[:3]) and torch.equal(step.q_out, step.q)
+    assert c.status.item() == 0
+
+
 def test_far_positions():
     """Positions up to 2^31 - 1: an angle of 2 x 10^9 radians still has its 20 bits behind the point."""
     c = Cache([64], 4, 4, 64, seed=3)

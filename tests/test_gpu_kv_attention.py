@@ -74,6 +74,44 @@ def test_few_rows_split_over_the_gpu(lengths, e4m3):
     check(c, lengths, queries(c, len(lengths)), 128 ** -0.5, mass=True)
 
 
+@pytest.mark.parametrize("n_seqs", [32, 33, 128, 129, 257])
+def test_counts_of_sequences_around_the_ways_to_find_a_place(n_seqs):
+    lengths = [0 if i % 5 == 3 else (i * 977) % 301 for i in range(n_seqs)]
+    c = Cache(lengths, 6, 2, 64, 16, seed=n_seqs)
+    check(c, lengths, queries(c, n_seqs), 0.125, mass=True)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_scores_of_a_hundred_million(e4m3):
+    """Neighbouring fp32 scores are 16 apart there: a weight of 2^16 would not fit f16."""
+    c = Cache([200], 8, 1, 64, 16, e4m3, seed=21)
+    q = torch.zeros(1, 8, 64, device="cuda")
+    q[:, :, 0] = 2.0 ** 20
+    q = q.to(torch.bfloat16)
+    at = c.place(0, torch.arange(200, device="cuda"))
+    x = torch.zeros(200, 1, 64, device="cuda")
+    x[:, 0, 0] = torch.randint(90, 129, (200,), device="cuda").float()
+    c.k[at] = c.stored(x * c.k_scale, c.k_scale)  # whole numbers in steps of 8 in E4M3, exact in bf16 (up to 128)
+    out, lse = call(c, q, 1.0 / c.k_scale)
+    k = c.values(c.k, 0, 200)[:, 0, 0] * (1.0 if e4m3 else c.k_scale)
+    best = k == k.max()
+    want = (c.values(c.v, 0, 200)[best, 0] * c.v_scale).mean(0)  # the others weigh nothing: e^-1000000
+    bound = want.abs() * 2.0 ** -8 + 2.0 ** -10 * (c.values(c.v, 0, 200)[:, 0] * c.v_scale).abs().amax(0)
+    assert torch.isfinite(out).all() and ((out[0].double() - want).abs() <= bound).all()
+    top = k.max() * 2.0 ** 20 * (c.k_scale if e4m3 else 1.0) / c.k_scale
+    assert ((lse.double() - top).abs() <= top * 2.0 ** -20).all()
+
+
+def test_without_pools_of_weights_and_without_lse():
+    c = Cache([40, 3], 4, 2, 128, 16, seed=22, meta=False)
+    q, kv = queries(c, 2), c.kv()
+    out = torch.empty_like(q)
+    ft.ft_kv_attention(kv, q, 0.1, out, None, c.workspace(kv))
+    assert torch.equal(out, call(c, q, 0.1)[0])
+    with pytest.raises(ft.FtError, match="mass"):
+        ft.ft_kv_attention(kv, q, 0.1, out, None, c.workspace(kv), ft.FT_KV_MASS)
+
+
 def test_thousands_of_sequences():
     lengths = [(i * 7919) % 41 for i in range(3001)]
     c = Cache(lengths, 4, 2, 64, 16, seed=4)
