@@ -237,7 +237,7 @@ extern "C" ft_status ft_kv_attention(const ft_kv_cache* kv, const void* q, int64
   KV_TRY(sm_count(at.device, sms));
   const ft::KvAttnArgs a{view(*kv), (const uint16_t*)q, q_stride, scale, (uint16_t*)out, lse, (uint8_t*)workspace,
                          (flags & FT_KV_MASS) != 0};
-  return cu("ft_kv_attention", ft::launch_kv_attention(a, kv->format == FT_KV_E4M3, sms, (cudaStream_t)stream));
+  return cu("ft_kv_attention", ft::launch_kv_attention(a, kv->format == FT_KV_E4M3, at.device, sms, (cudaStream_t)stream));
 }
 
 extern "C" ft_status ft_kv_evict(const ft_kv_cache* kv, const int32_t* budgets, int32_t recent, void* workspace,
@@ -255,7 +255,7 @@ extern "C" ft_status ft_kv_evict(const ft_kv_cache* kv, const int32_t* budgets, 
   int sms = 0;
   KV_TRY(sm_count(at.device, sms));
   const ft::KvEvictArgs a{view(*kv), budgets, recent, (uint8_t*)workspace};
-  return cu("ft_kv_evict", ft::launch_kv_evict(a, kv->head_dim * element_size(*kv), sms, (cudaStream_t)stream));
+  return cu("ft_kv_evict", ft::launch_kv_evict(a, kv->head_dim * element_size(*kv), at.device, sms, (cudaStream_t)stream));
 }
 
 extern "C" ft_status ft_kv_sync_status(const ft_kv_cache* kv, void* stream) {

@@ -2,6 +2,8 @@
 // ft_kv_attention.cu, ft_kv_evict.cu) and the host calls of ft_kv.cu.
 #pragma once
 
+#include <atomic>
+
 #include "ft_common.cuh"
 
 namespace ft {
@@ -88,8 +90,19 @@ int64_t kv_attn_workspace(const ft_kv_cache& c);
 int64_t kv_evict_workspace(const ft_kv_cache& c);
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool e4m3, bool adjacent, cudaStream_t s);
-cudaError_t launch_kv_attention(const KvAttnArgs& a, bool e4m3, int sms, cudaStream_t s);
-cudaError_t launch_kv_evict(const KvEvictArgs& a, int row_bytes, int sms, cudaStream_t s);
+cudaError_t launch_kv_attention(const KvAttnArgs& a, bool e4m3, int device, int sms, cudaStream_t s);
+cudaError_t launch_kv_evict(const KvEvictArgs& a, int row_bytes, int device, int sms, cudaStream_t s);
+
+// Sets a kernel attribute once on each device (`done` has a bit for each; a second thread
+// that sets it too does no harm).
+template <typename F>
+inline cudaError_t kv_attribute_once(std::atomic<uint64_t>& done, int device, F* kern, cudaFuncAttribute what, int value) {
+  const uint64_t bit = (uint64_t)1 << (device & 63);
+  if (device < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, what, value);
+  if (e == cudaSuccess && device < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Launch with programmatic stream serialisation: the kernel may start while
 // its predecessor on the stream still runs.  Every thread of every kernel here executes

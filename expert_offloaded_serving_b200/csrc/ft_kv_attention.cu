@@ -971,7 +971,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) k_kv_join(JoinArgs args) {
 }
 
 template <int D, bool E4M3, int NB, bool MASS>
-cudaError_t run(SplitArgs& a, int sms, cudaStream_t s) {
+cudaError_t run(SplitArgs& a, int device, int sms, cudaStream_t s) {
   using R = Ring<D * (E4M3 ? 1 : 2)>;
   static_assert(R::kStages >= 2 && R::kWarps <= kMaxWarps, "a ring of at least two stages fits");
   static_assert(R::kTile == tile_of(D * (E4M3 ? 1 : 2)), "the workspace is carved for this tile");
@@ -986,7 +986,8 @@ cudaError_t run(SplitArgs& a, int sms, cudaStream_t s) {
       encode_tmap_rows(&a.v_map, kv.v, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift, deep) != FT_OK)
     return cudaErrorInvalidValue;
   auto kern = k_kv_split<D, E4M3, NB, MASS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = kv_attribute_once(done, device, kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kBytes);
   if (e != cudaSuccess) return e;
   if ((e = kv_launch_after(kern, dim3((unsigned)sms), R::kWarps * 32, R::kBytes, s, a)) != cudaSuccess) return e;
   const JoinArgs ja{a.a, a.w, a.groups};
@@ -994,9 +995,9 @@ cudaError_t run(SplitArgs& a, int sms, cudaStream_t s) {
 }
 
 template <int D, bool E4M3>
-cudaError_t run_d(SplitArgs& a, int sms, cudaStream_t s) {
-  if (a.a.kv.G > 8) return a.a.mass ? run<D, E4M3, 2, true>(a, sms, s) : run<D, E4M3, 2, false>(a, sms, s);
-  return a.a.mass ? run<D, E4M3, 1, true>(a, sms, s) : run<D, E4M3, 1, false>(a, sms, s);
+cudaError_t run_d(SplitArgs& a, int device, int sms, cudaStream_t s) {
+  if (a.a.kv.G > 8) return a.a.mass ? run<D, E4M3, 2, true>(a, device, sms, s) : run<D, E4M3, 2, false>(a, device, sms, s);
+  return a.a.mass ? run<D, E4M3, 1, true>(a, device, sms, s) : run<D, E4M3, 1, false>(a, device, sms, s);
 }
 
 }  // namespace
@@ -1007,7 +1008,7 @@ int64_t kv_attn_workspace(const ft_kv_cache& c) {
                c.n_pages * c.n_kv_heads * c.page_size, c.mass != nullptr);
 }
 
-cudaError_t launch_kv_attention(const KvAttnArgs& args, bool e4m3, int sms, cudaStream_t s) {
+cudaError_t launch_kv_attention(const KvAttnArgs& args, bool e4m3, int device, int sms, cudaStream_t s) {
   SplitArgs a;
   a.a = args;
   a.groups = (args.kv.G + kRows - 1) / kRows;
@@ -1016,11 +1017,11 @@ cudaError_t launch_kv_attention(const KvAttnArgs& args, bool e4m3, int sms, cuda
         (int64_t)kv.n_pages * kv.Hkv << kv.page_shift, args.mass);
   sms = sms < kKvMaxSms ? sms : kKvMaxSms;
   switch (kv.D) {
-    case 64: return e4m3 ? run_d<64, true>(a, sms, s) : run_d<64, false>(a, sms, s);
-    case 96: return e4m3 ? run_d<96, true>(a, sms, s) : run_d<96, false>(a, sms, s);
-    case 128: return e4m3 ? run_d<128, true>(a, sms, s) : run_d<128, false>(a, sms, s);
-    case 192: return e4m3 ? run_d<192, true>(a, sms, s) : run_d<192, false>(a, sms, s);
-    default: return e4m3 ? run_d<256, true>(a, sms, s) : run_d<256, false>(a, sms, s);
+    case 64: return e4m3 ? run_d<64, true>(a, device, sms, s) : run_d<64, false>(a, device, sms, s);
+    case 96: return e4m3 ? run_d<96, true>(a, device, sms, s) : run_d<96, false>(a, device, sms, s);
+    case 128: return e4m3 ? run_d<128, true>(a, device, sms, s) : run_d<128, false>(a, device, sms, s);
+    case 192: return e4m3 ? run_d<192, true>(a, device, sms, s) : run_d<192, false>(a, device, sms, s);
+    default: return e4m3 ? run_d<256, true>(a, device, sms, s) : run_d<256, false>(a, device, sms, s);
   }
 }
 

@@ -447,9 +447,10 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv_move(SelectArgs args) {
 }
 
 template <int N, bool ONE>
-cudaError_t select(const SelectArgs& a, int blocks, cudaStream_t s) {
+cudaError_t select(const SelectArgs& a, int blocks, int device, cudaStream_t s) {
   auto kern = k_kv_select<N, ONE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = kv_attribute_once(done, device, kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.items * blocks));
@@ -473,7 +474,7 @@ int64_t kv_evict_workspace(const ft_kv_cache& c) {
   return carve(w, nullptr, c.n_seqs, c.n_kv_heads, c.n_pages * c.n_kv_heads * c.page_size);
 }
 
-cudaError_t launch_kv_evict(const KvEvictArgs& args, int row_bytes, int sms, cudaStream_t s) {
+cudaError_t launch_kv_evict(const KvEvictArgs& args, int row_bytes, int device, int sms, cudaStream_t s) {
   const KvView& kv = args.kv;
   SelectArgs a;
   a.a = args;
@@ -487,12 +488,12 @@ cudaError_t launch_kv_evict(const KvEvictArgs& args, int row_bytes, int sms, cud
   // Entries of a thread, by the longest sequence the table has room for: all of them in
   // registers where they are 32 at most.
   const int share = (kv.cap + blocks - 1) / blocks, each = (share + kSelThreads - 1) / kSelThreads;
-  cudaError_t e = each <= 4    ? select<4, true>(a, blocks, s)
-                  : each <= 8  ? select<8, true>(a, blocks, s)
-                  : each <= 16 ? select<16, true>(a, blocks, s)
-                  : each <= 20 ? select<20, true>(a, blocks, s)
-                  : each <= 32 ? select<32, true>(a, blocks, s)
-                               : select<16, false>(a, blocks, s);
+  cudaError_t e = each <= 4    ? select<4, true>(a, blocks, device, s)
+                  : each <= 8  ? select<8, true>(a, blocks, device, s)
+                  : each <= 16 ? select<16, true>(a, blocks, device, s)
+                  : each <= 20 ? select<20, true>(a, blocks, device, s)
+                  : each <= 32 ? select<32, true>(a, blocks, device, s)
+                               : select<16, false>(a, blocks, device, s);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)(sms * 4));  // all resident: 64 registers a thread
   switch (row_bytes) {
