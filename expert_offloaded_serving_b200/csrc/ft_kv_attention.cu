@@ -43,8 +43,6 @@ namespace ft {
 namespace {
 
 constexpr int kRows = 16;        // query heads of an item: rows of the mma tile
-constexpr int kMaxWarps = 8;      // warps of a block at most
-constexpr int kMaxChunks = kKvMaxSms * kMaxWarps;
 
 // The ring of a warp for entries of RB bytes a side: a stage holds a tile of keys
 // and one of values as TMA leaves them, boxes of kBox bytes x the tile's rows whose
@@ -56,21 +54,22 @@ constexpr int kMaxChunks = kKvMaxSms * kMaxWarps;
 // There 4 warps x 3 stages match 6 x 2 on long rows (93 and 92 us) and win on 64 sequences of 200
 // entries (12.4 against 15.3); rows of 128 bytes want 8 warps (a ragged batch 56.8 us, 59.7 with
 // 6); beyond 256 the registers of O leave room for 4.
+constexpr int tile_of(int row_bytes) { return row_bytes <= 256 ? 32 : 16; }
+constexpr int warps_of(int row_bytes) { return row_bytes >= 256 ? 4 : 8; }
 template <int RB>
 struct Ring {
-  static constexpr int kTile = RB <= 256 ? 32 : 16;  // entries
+  static constexpr int kTile = tile_of(RB);  // entries
   static constexpr int kBox = RB % 128 == 0 ? 128 : RB % 64 == 0 ? 64 : 32;
   static constexpr int kBoxes = RB / kBox;
   static constexpr int kBoxBytes = kTile * kBox;
   static constexpr int kSide = kTile * RB;
   static constexpr int kStage = 2 * kSide;
-  static constexpr int kWarps = RB >= 256 ? 4 : 8;
+  static constexpr int kWarps = warps_of(RB);
   static constexpr int kFit = 220 * 1024 / (kWarps * kStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kBytes = kWarps * kStages * kStage + 1024;  // the swizzle goes by address: aligned to its period
 };
 
-constexpr int tile_of(int row_bytes) { return row_bytes <= 256 ? 32 : 16; }
 
 // What chunk j leaves for block j of k_kv_join.
 struct __align__(16) Chunk {
@@ -82,8 +81,8 @@ struct __align__(16) Chunk {
 };
 struct AttnWork {
   Chunk* chunks;
-  float2* ml;        // [chunks][2][16] m and l of a part (log2 units); side 0: a row that came in, 1: one that goes on
-  float* o;          // [chunks][2][16][D]
+  float2* ml;        // [chunks][2][8 or 16] m and l of a part (log2 units); side 0: a row that came in, 1: one that goes on
+  float* o;          // [chunks][2][8 or 16][D]
   float* lse2;       // [n_seqs][Hq] lse of whole rows in log2 units (mass)
   float* scores;     // [tiles][entries of a tile][8 or 16 rows] scores in log2 units (mass)
   int64_t tiles;     // that `scores` holds
@@ -93,14 +92,15 @@ __host__ __device__ inline int64_t up256(int64_t n) { return (n + 255) & ~(int64
 
 // Scores of the tiles that sequences of their own pages can have: every row of the pool, and a last tile each.
 inline int64_t carve(AttnWork& w, uint8_t* base, int D, int row_bytes, int n_seqs, int Hq, int Hkv, int64_t rows, bool mass) {
-  const int G = Hq / Hkv, tile = tile_of(row_bytes);
+  const int G = Hq / Hkv, tile = tile_of(row_bytes), kept = G > 8 ? 16 : 8;  // rows of an item
+  const int64_t chunks = kKvMaxSms * warps_of(row_bytes);
   int64_t at = 0;
   w.chunks = reinterpret_cast<Chunk*>(base + at);
-  at += up256((int64_t)kMaxChunks * sizeof(Chunk));
+  at += up256(chunks * (int64_t)sizeof(Chunk));
   w.ml = reinterpret_cast<float2*>(base + at);
-  at += up256((int64_t)kMaxChunks * 2 * kRows * sizeof(float2));
+  at += up256(chunks * 2 * kept * (int64_t)sizeof(float2));
   w.o = reinterpret_cast<float*>(base + at);
-  at += up256((int64_t)kMaxChunks * 2 * kRows * D * sizeof(float));
+  at += up256(chunks * 2 * kept * D * (int64_t)sizeof(float));
   w.lse2 = reinterpret_cast<float*>(base + at);
   w.scores = nullptr;
   w.tiles = 0;
@@ -108,7 +108,7 @@ inline int64_t carve(AttnWork& w, uint8_t* base, int D, int row_bytes, int n_seq
   at += up256((int64_t)n_seqs * Hq * sizeof(float));
   w.scores = reinterpret_cast<float*>(base + at);
   w.tiles = (rows / tile + (int64_t)n_seqs * Hkv) * ((G + kRows - 1) / kRows);
-  at += up256(w.tiles * tile * (G > 8 ? 16 : 8) * (int64_t)sizeof(float));
+  at += up256(w.tiles * tile * kept * (int64_t)sizeof(float));
   return at;
 }
 
@@ -214,9 +214,9 @@ __device__ __forceinline__ int tiles_of(int len) {
 template <int TILE>
 __device__ __forceinline__ void next_sequence(const KvView& kv, Place& p) {
   do {
-    p.b++;
-    p.len = p.b < kv.n_seqs ? kv_length(kv, p.b) : 1;
+    p.len = ++p.b < kv.n_seqs ? kv_length(kv, p.b) : 1;
   } while (p.len == 0);
+  p.b = min(p.b, kv.n_seqs - 1);  // past the end only if somebody changes the lengths meanwhile
   p.nt = tiles_of<TILE>(p.len);
 }
 
@@ -352,11 +352,17 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     }
     base = s_sum[l];
     cons.b = l * per;
-    for (; lo < hi; cons.b++) {
+    cons.len = 0;
+    for (; lo < hi && cons.b < kv.n_seqs; cons.b++) {
       cons.len = kv_length(kv, cons.b);
       const int n = tiles_of<TILE>(cons.len) * items;
       if (lo < base + n) break;
       base += n;
+    }
+    if (cons.b >= kv.n_seqs || cons.len == 0) {  // only if somebody changes the lengths meanwhile
+      cons.b = kv.n_seqs - 1;
+      cons.len = 1;
+      base = lo;
     }
   }
   // Idle rows, from the last warps on, which have no tiles in a small batch: out 0, lse -inf.
@@ -389,7 +395,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
   const int box_shift = args.box_shift, box_bytes = RB << box_shift;
   auto box_row = [&](const Place& p) {  // first row of the lane's box, -1 where there is none
     const int slot = p.t * TILE + (lane << box_shift);
-    return lane < (TILE >> box_shift) && slot < p.len && p.b < kv.n_seqs ? kv_row(kv, p.b, p.hh / args.groups, slot) : -1;
+    return lane < (TILE >> box_shift) && slot < p.len ? kv_row(kv, p.b, p.hh / args.groups, slot) : -1;
   };
   int row_next = box_row(prod), left_next = prod.len - prod.t * TILE;
   int to_load = hi - lo;
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
             if (MASS) args.w.lse2[(int64_t)b * kv.Hq + head0 + row] = lse2;
           }
         } else {
-          const int64_t at = ((int64_t)j * 2 + side) * kRows + row;
+          const int64_t at = ((int64_t)j * 2 + side) * (8 * NB) + row;
           if (g == 0) args.w.ml[at] = make_float2(m[nb][i], sum);
           float* po = args.w.o + at * D;
 #pragma unroll
@@ -544,8 +550,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
 
   // ldmatrix addresses: lanes 0-7, 8-15, 16-23 and 24-31 point at the rows of the four
   // 8 x 8 matrices, by halves of the entries first, or (values of a BF16 cache) of the
-  // dims.  `column` 16-byte pieces from the row's begin; the swizzle flips the piece's low
-  // bits by the row's.
+  // dims.  The swizzle flips the low bits of a 16-byte piece's number by the row's.
   constexpr uint32_t kFlip = R::kBox == 128 ? 7 : R::kBox == 64 ? 3 : 1, kFlipShift = R::kBox == 128 ? 0 : R::kBox == 64 ? 1 : 2;
   const uint32_t row_e = lane & 15, col_e = lane >> 4, row_d = (lane & 7) + ((lane >> 4) << 3), col_d = (lane >> 3) & 1;
   const uint32_t by_entry = row_e * R::kBox + ((col_e ^ ((row_e >> kFlipShift) & kFlip)) << 4);
@@ -772,7 +777,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
         stage = 0;
         phase ^= 1u;
       }
-      if (i < R::kStages) wait_full(full + stage, phase);
+      wait_full(full + stage, phase);
     }
     left.tiles = 0;
     left.go_b = -1;
@@ -804,7 +809,7 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 // What a sum with reference x counts for under the reference `both` >= x.
 __device__ __forceinline__ float rescale(float x, float both) { return x == both ? 1.0f : exp2_fast(x - both); }
 
-template <int D>
+template <int D, int NB>
 __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
   const KvView& kv = args.a.kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -833,7 +838,7 @@ __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
     };
 #pragma unroll 8
     for (int p = lane / width; p < parts; p += split) {
-      const int64_t at = ((int64_t)(c.go_j0 + p) * 2 + (p == 0 ? 1 : 0)) * kRows + row;
+      const int64_t at = ((int64_t)(c.go_j0 + p) * 2 + (p == 0 ? 1 : 0)) * (8 * NB) + row;
       const float2 ml = args.w.ml[at];
       add(ml.x, ml.y, *reinterpret_cast<const float4*>(args.w.o + at * D + d4 * 4));
     }
@@ -896,7 +901,7 @@ __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
           z[i] = sub * 4 + i < n_rows ? args.w.lse2[(int64_t)p.b * kv.Hq + h * kv.G + gi * kRows + sub * 4 + i] : kNegInf;
       } else {
         auto part = [&](int q, float (&m)[4], float (&l)[4]) {
-          const float4* ml = reinterpret_cast<const float4*>(args.w.ml + ((int64_t)(j0 + q) * 2 + (q == 0 ? 1 : 0)) * kRows + sub * 4);
+          const float4* ml = reinterpret_cast<const float4*>(args.w.ml + ((int64_t)(j0 + q) * 2 + (q == 0 ? 1 : 0)) * (8 * NB) + sub * 4);
           const float4 u = ml[0], v = ml[1];
           m[0] = u.x, l[0] = u.y, m[1] = u.z, l[1] = u.w, m[2] = v.x, l[2] = v.y, m[3] = v.z, l[3] = v.w;
         };
@@ -966,15 +971,14 @@ __global__ void __launch_bounds__(kJoinThreads, 8) k_kv_join(JoinArgs args) {
   kv_pdl_trigger();
   kv_pdl_wait();
   const Chunk c = args.w.chunks[blockIdx.x];
-  if (c.go_b >= 0) join_row<D>(args, c);
+  if (c.go_b >= 0) join_row<D, NB>(args, c);
   if (MASS && c.tiles > 0) add_mass<TILE, NB>(args, c);
 }
 
 template <int D, bool E4M3, int NB, bool MASS>
 cudaError_t run(SplitArgs& a, int device, int sms, cudaStream_t s) {
   using R = Ring<D * (E4M3 ? 1 : 2)>;
-  static_assert(R::kStages >= 2 && R::kWarps <= kMaxWarps, "a ring of at least two stages fits");
-  static_assert(R::kTile == tile_of(D * (E4M3 ? 1 : 2)), "the workspace is carved for this tile");
+  static_assert(R::kStages >= 2, "a ring of at least two stages fits");
   const KvView& kv = a.a.kv;
   const uint64_t rows = (uint64_t)kv.n_pages * kv.Hkv << kv.page_shift;
   a.box_shift = R::kTile == 32 ? 5 : 4;
