@@ -803,13 +803,15 @@ struct JoinArgs {
   int groups;
 };
 
-constexpr int kJoinThreads = 128;
-constexpr int kJoinWarps = kJoinThreads / 32;
+// Warps of a block of k_kv_join: 32 an SM in all, as many blocks as the split has warps.  Measured
+// against half and double: 37 entries 6.6 us with 8 (4: 7.3, 16: 6.8), a weighed E4M3 batch 56.8
+// with 4 (2: 58.9, 8: 60.6).
+constexpr int join_warps(int row_bytes) { return 32 / warps_of(row_bytes); }
 
 // What a sum with reference x counts for under the reference `both` >= x.
 __device__ __forceinline__ float rescale(float x, float both) { return x == both ? 1.0f : exp2_fast(x - both); }
 
-template <int D, int NB>
+template <int D, int NB, int WARPS>
 __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
   const KvView& kv = args.a.kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -819,11 +821,11 @@ __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
   const int parts = c.go_parts, blocks = parts - 1, mine = (int)blockIdx.x - c.go_j0;
   // Units of four dims of a row.  `split` lanes share a unit's parts while
   // there are more threads than units.
-  const int units = n_rows * (D / 4), threads = blocks * kJoinThreads;
+  const int units = n_rows * (D / 4), threads = blocks * WARPS * 32;
   int split = 1;
   while (split < 32 && split * 2 <= parts && units * split * 2 <= threads) split *= 2;
   const int width = 32 / split;
-  for (int u0 = (mine * kJoinWarps + warp) * width; u0 < units; u0 += blocks * kJoinWarps * width) {
+  for (int u0 = (mine * WARPS + warp) * width; u0 < units; u0 += blocks * WARPS * width) {
     const int u = min(u0 + lane % width, units - 1), row = u / (D / 4), d4 = u - row * (D / 4);
     float top = kNegInf, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -860,12 +862,12 @@ __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
 // The warp's share of a chunk's tiles.  L lanes hold an entry's 8 NB scores, four
 // query heads each; 32 / L entries go at a time, and after L of them each lane
 // has the sum of one entry.
-template <int TILE, int NB>
+template <int TILE, int NB, int WARPS>
 __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
   constexpr int L = 2 * NB, E = 32 / L;
   const KvView& kv = args.a.kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L, set = lane / L;
-  const int items = kv.Hkv * args.groups, share = (c.tiles + kJoinWarps - 1) / kJoinWarps;
+  const int items = kv.Hkv * args.groups, share = (c.tiles + WARPS - 1) / WARPS;
   const int chunk0 = (int)blockIdx.x * c.size, lo = chunk0 + min(c.tiles, warp * share), hi = min(chunk0 + c.tiles, lo + share);
   Place p{c.b, c.hh, 0, c.len, tiles_of<TILE>(c.len)};
   for (int first = c.first; first < hi;) {
@@ -966,13 +968,13 @@ __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
   }
 }
 
-template <int D, int TILE, int NB, bool MASS>
-__global__ void __launch_bounds__(kJoinThreads, 8) k_kv_join(JoinArgs args) {
+template <int D, int TILE, int NB, bool MASS, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) k_kv_join(JoinArgs args) {
   kv_pdl_trigger();
   kv_pdl_wait();
   const Chunk c = args.w.chunks[blockIdx.x];
-  if (c.go_b >= 0) join_row<D, NB>(args, c);
-  if (MASS && c.tiles > 0) add_mass<TILE, NB>(args, c);
+  if (c.go_b >= 0) join_row<D, NB, WARPS>(args, c);
+  if (MASS && c.tiles > 0) add_mass<TILE, NB, WARPS>(args, c);
 }
 
 template <int D, bool E4M3, int NB, bool MASS>
@@ -995,7 +997,8 @@ cudaError_t run(SplitArgs& a, int device, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if ((e = kv_launch_after(kern, dim3((unsigned)sms), R::kWarps * 32, R::kBytes, s, a)) != cudaSuccess) return e;
   const JoinArgs ja{a.a, a.w, a.groups};
-  return kv_launch_after(k_kv_join<D, R::kTile, NB, MASS>, dim3((unsigned)(sms * R::kWarps)), kJoinThreads, 0, s, ja);
+  constexpr int JW = join_warps(D * (E4M3 ? 1 : 2));
+  return kv_launch_after(k_kv_join<D, R::kTile, NB, MASS, JW>, dim3((unsigned)(sms * R::kWarps)), JW * 32, 0, s, ja);
 }
 
 template <int D, bool E4M3>
