@@ -26,8 +26,8 @@
 // valid when lengths grow, and the split depends on nothing but the lengths and the
 // number of SMs.
 //
-// With FT_KV_MASS the scores go to the workspace as they come (8 or 16 fp32 values an entry,
-// next to its 4 D or 2 D bytes), and k_kv_join turns them into weights once the row's lse
+// With FT_KV_MASS the scores go to the workspace as they come (G fp32 values an entry, next to
+// its 4 D or 2 D bytes), and k_kv_join turns them into weights once the row's lse
 // is known.
 //
 // Measured (one B200, a graph of passes): 1 x 131,071 entries, 64 query and 8 KV heads of 128, BF16
@@ -84,11 +84,14 @@ struct AttnWork {
   float2* ml;        // [chunks][2][8 or 16] m and l of a part (log2 units); side 0: a row that came in, 1: one that goes on
   float* o;          // [chunks][2][8 or 16][D]
   float* lse2;       // [n_seqs][Hq] lse of whole rows in log2 units (mass)
-  float* scores;     // [tiles][entries of a tile][8 or 16 rows] scores in log2 units (mass)
+  float* scores;     // [tiles][entries of a tile][score_rows] scores in log2 units (mass)
   int64_t tiles;     // that `scores` holds
 };
 
 __host__ __device__ inline int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
+
+// Scores kept of an entry, for G query heads a KV head: as many of the 8 or 16 rows of an item as a power of two covers.
+__host__ __device__ inline int score_rows(int G) { return G > 8 ? 16 : G > 4 ? 8 : G > 2 ? 4 : G; }
 
 // Scores of the tiles that sequences of their own pages can have: every row of the pool, and a last tile each.
 inline int64_t carve(AttnWork& w, uint8_t* base, int D, int row_bytes, int n_seqs, int Hq, int Hkv, int64_t rows, bool mass) {
@@ -108,7 +111,7 @@ inline int64_t carve(AttnWork& w, uint8_t* base, int D, int row_bytes, int n_seq
   at += up256((int64_t)n_seqs * Hq * sizeof(float));
   w.scores = reinterpret_cast<float*>(base + at);
   w.tiles = (rows / tile + (int64_t)n_seqs * Hkv) * ((G + kRows - 1) / kRows);
-  at += up256(w.tiles * tile * kept * (int64_t)sizeof(float));
+  at += up256(w.tiles * tile * score_rows(G) * (int64_t)sizeof(float));
   return at;
 }
 
@@ -664,14 +667,22 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
         over |= x - m[nb][i] > kSlack;  // the difference is exact where the two are near
       }
     if (MASS && at < args.w.tiles) {
-      float* sc = args.w.scores + ((int64_t)at * TILE + g) * (8 * NB) + j2;
+      const int kept = NB == 2 ? 16 : score_rows(kv.G);  // of an entry
+      float* sc = args.w.scores + ((int64_t)at * TILE + g) * kept + j2;
 #pragma unroll
       for (int t = 0; t < NT; t++)
 #pragma unroll
-        for (int e = 0; e < 2; e++)
+        for (int e = 0; e < 2; e++) {
+          float* const to = sc + (16 * t + 8 * e) * kept;
+          if (NB == 1 && kept == 1) {
+            if (j2 == 0) *to = s[t][0][2 * e];
+            continue;
+          }
+          if (NB == 1 && j2 >= kept) continue;
 #pragma unroll
           for (int nb = 0; nb < NB; nb++)
-            *reinterpret_cast<float2*>(sc + (16 * t + 8 * e) * (8 * NB) + 8 * nb) = make_float2(s[t][nb][2 * e], s[t][nb][2 * e + 1]);
+            *reinterpret_cast<float2*>(to + 8 * nb) = make_float2(s[t][nb][2 * e], s[t][nb][2 * e + 1]);
+        }
     }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -859,12 +870,33 @@ __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
   }
 }
 
-// The warp's share of a chunk's tiles.  L lanes hold an entry's 8 NB scores, four
-// query heads each; 32 / L entries go at a time, and after L of them each lane
-// has the sum of one entry.
-template <int TILE, int NB, int WARPS>
+template <int V>
+struct Floats;
+template <>
+struct Floats<1> {
+  using type = float;
+};
+template <>
+struct Floats<2> {
+  using type = float2;
+};
+template <>
+struct Floats<4> {
+  using type = float4;
+};
+
+// The warp's share of a chunk's tiles.  L lanes hold an entry's KEPT scores, V query heads
+// each; 32 / L entries go at a time, and after L of them each lane has the sum
+// of one entry.
+template <int TILE, int KEPT, int WARPS>
 __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
-  constexpr int L = 2 * NB, E = 32 / L;
+  constexpr int ROWS = KEPT == 16 ? 16 : 8, V = KEPT < 4 ? KEPT : 4, L = KEPT / V, E = 32 / L;
+  constexpr int RUNS = L == 1 ? 4 : 2;  // of 32 entries, their loads in flight together
+  using Vec = typename Floats<V>::type;
+  union Scores {
+    Vec vec;
+    float v[V];
+  };
   const KvView& kv = args.a.kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L, set = lane / L;
   const int items = kv.Hkv * args.groups, share = (c.tiles + WARPS - 1) / WARPS;
@@ -878,85 +910,94 @@ __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
     for (int gi = 0; counts && gi < args.groups; gi++) {
       const int row_first = first + gi * p.nt, j0 = row_first / c.size;
       const int parts = (row_first + p.nt - 1) / c.size - j0 + 1, n_rows = min(kRows, kv.G - gi * kRows);
-      const float* const scores = args.w.scores + (int64_t)row_first * TILE * (8 * NB) + sub * 4;
+      const float* const scores = args.w.scores + (int64_t)row_first * TILE * KEPT + sub * V;
       const int last = (int)min((int64_t)e1, (args.w.tiles - row_first) * TILE);  // entries whose scores were kept
-      float4 x[2][L];
-      int row[2];
-      auto load = [&](int e) {  // two runs of 32 entries; the lane keeps the sum of entry sub * E + set of each
+      Scores x[RUNS][L];
+      int row[RUNS];
+      auto load = [&](int e) {  // the lane keeps the sum of entry sub * E + set of each run
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-          const int own = e + 32 * r + sub * E + set;
-          row[r] = own < last ? kv_row(kv, p.b, h, own) : -1;
+        for (int r = 0; r < RUNS; r++)
 #pragma unroll
           for (int k = 0; k < L; k++) {
             const int at = e + 32 * r + k * E + set;
-            x[r][k] = at < last ? *reinterpret_cast<const float4*>(scores + (int64_t)at * (8 * NB))
-                                : make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+#pragma unroll
+            for (int i = 0; i < V; i++) x[r][k].v[i] = kNegInf;
+            if (at < last) x[r][k].vec = *reinterpret_cast<const Vec*>(scores + (int64_t)at * KEPT);
           }
+#pragma unroll
+        for (int r = 0; r < RUNS; r++) {
+          const int own = e + 32 * r + sub * E + set;
+          row[r] = own < last ? kv_row(kv, p.b, h, own) : -1;
         }
       };
       if (e0 < last) load(e0);
-      float z[4];  // lse of the lane's heads; +inf takes a head (without weights, or none) out
+      float z[V];  // lse of the lane's heads; +inf takes a head (without weights, or none) out
       if (parts == 1) {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-          z[i] = sub * 4 + i < n_rows ? args.w.lse2[(int64_t)p.b * kv.Hq + h * kv.G + gi * kRows + sub * 4 + i] : kNegInf;
+        for (int i = 0; i < V; i++)
+          z[i] = sub * V + i < n_rows ? args.w.lse2[(int64_t)p.b * kv.Hq + h * kv.G + gi * kRows + sub * V + i] : kNegInf;
       } else {
-        auto part = [&](int q, float (&m)[4], float (&l)[4]) {
-          const float4* ml = reinterpret_cast<const float4*>(args.w.ml + ((int64_t)(j0 + q) * 2 + (q == 0 ? 1 : 0)) * (8 * NB) + sub * 4);
-          const float4 u = ml[0], v = ml[1];
-          m[0] = u.x, l[0] = u.y, m[1] = u.z, l[1] = u.w, m[2] = v.x, l[2] = v.y, m[3] = v.z, l[3] = v.w;
-        };
-        float top[4], sum[4] = {}, m[4], l[4];
-        part(min(set, parts - 1), m, l);
+        auto part = [&](int q, float2 (&ml)[V]) {
+          const float2* at = args.w.ml + ((int64_t)(j0 + q) * 2 + (q == 0 ? 1 : 0)) * ROWS + sub * V;
+          if constexpr (V == 4) {
+            const float4 u = reinterpret_cast<const float4*>(at)[0], v = reinterpret_cast<const float4*>(at)[1];
+            ml[0] = make_float2(u.x, u.y), ml[1] = make_float2(u.z, u.w);
+            ml[2] = make_float2(v.x, v.y), ml[3] = make_float2(v.z, v.w);
+          } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          top[i] = m[i];
-          if (set >= parts) l[i] = 0.0f;
+            for (int i = 0; i < V; i++) ml[i] = at[i];
+          }
+        };
+        float2 ml[V];
+        part(min(set, parts - 1), ml);
+        if (set >= parts) {
+#pragma unroll
+          for (int i = 0; i < V; i++) ml[i].y = 0.0f;
         }
         for (int q = set + E; q < parts; q += E) {
-          float mq[4], lq[4];
-          part(q, mq, lq);
+          float2 y[V];
+          part(q, y);
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const float both = fmaxf(top[i], mq[i]);
-            l[i] = l[i] * rescale(top[i], both) + lq[i] * rescale(mq[i], both);
-            top[i] = both;
+          for (int i = 0; i < V; i++) {
+            const float both = fmaxf(ml[i].x, y[i].x);
+            ml[i].y = ml[i].y * rescale(ml[i].x, both) + y[i].y * rescale(y[i].x, both);
+            ml[i].x = both;
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          m[i] = top[i];
+        for (int i = 0; i < V; i++) {
+          float top = ml[i].x;
 #pragma unroll
-          for (int d = L; d < 32; d <<= 1) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], d));
-          sum[i] = l[i] * rescale(m[i], top[i]);
+          for (int d = L; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          float sum = ml[i].y * rescale(ml[i].x, top);
 #pragma unroll
-          for (int d = L; d < 32; d <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
-          z[i] = sub * 4 + i < n_rows && sum[i] != 0.0f ? top[i] + __log2f(sum[i]) : kNegInf;
+          for (int d = L; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          z[i] = sub * V + i < n_rows && sum != 0.0f ? top + __log2f(sum) : kNegInf;
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; i++)
+      for (int i = 0; i < V; i++)
         if (z[i] == kNegInf) z[i] = -kNegInf;
 #pragma unroll 1
       for (int e = e0; e < last;) {
-        float old[2];
+        float old[RUNS];
 #pragma unroll
-        for (int r = 0; r < 2; r++) old[r] = row[r] >= 0 ? kv.mass[row[r]] : 0.0f;
+        for (int r = 0; r < RUNS; r++) old[r] = row[r] >= 0 ? kv.mass[row[r]] : 0.0f;
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
+        for (int r = 0; r < RUNS; r++) {
           float mine = 0.0f;
 #pragma unroll
           for (int k = 0; k < L; k++) {
-            const float4 y = x[r][k];
-            float sum = (exp2_fast(y.x - z[0]) + exp2_fast(y.y - z[1])) + (exp2_fast(y.z - z[2]) + exp2_fast(y.w - z[3]));
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; i++) sum += exp2_fast(x[r][k].v[i] - z[i]);
 #pragma unroll
             for (int d = 1; d < L; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             if (sub == k) mine = sum;
           }
           if (row[r] >= 0) kv.mass[row[r]] = old[r] + mine;
         }
-        e += 64;
+        e += 32 * RUNS;
         if (e < last) load(e);
       }
     }
@@ -968,13 +1009,16 @@ __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
   }
 }
 
-template <int D, int TILE, int NB, bool MASS, int WARPS>
+// KEPT: scores of an entry (0: without FT_KV_MASS).
+template <int D, int TILE, int NB, int KEPT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) k_kv_join(JoinArgs args) {
   kv_pdl_trigger();
   kv_pdl_wait();
   const Chunk c = args.w.chunks[blockIdx.x];
   if (c.go_b >= 0) join_row<D, NB, WARPS>(args, c);
-  if (MASS && c.tiles > 0) add_mass<TILE, NB, WARPS>(args, c);
+  if constexpr (KEPT > 0) {
+    if (c.tiles > 0) add_mass<TILE, KEPT, WARPS>(args, c);
+  }
 }
 
 template <int D, bool E4M3, int NB, bool MASS>
@@ -997,8 +1041,18 @@ cudaError_t run(SplitArgs& a, int device, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if ((e = kv_launch_after(kern, dim3((unsigned)sms), R::kWarps * 32, R::kBytes, s, a)) != cudaSuccess) return e;
   const JoinArgs ja{a.a, a.w, a.groups};
-  constexpr int JW = join_warps(D * (E4M3 ? 1 : 2));
-  return kv_launch_after(k_kv_join<D, R::kTile, NB, MASS, JW>, dim3((unsigned)(sms * R::kWarps)), JW * 32, 0, s, ja);
+  constexpr int JW = join_warps(D * (E4M3 ? 1 : 2)), T = R::kTile;
+  const dim3 chunks((unsigned)(sms * R::kWarps));
+  auto join = [&](void (*kern)(const JoinArgs)) { return kv_launch_after(kern, chunks, JW * 32, 0, s, ja); };
+  if constexpr (!MASS) return join(k_kv_join<D, T, NB, 0, JW>);
+  else if constexpr (NB == 2) return join(k_kv_join<D, T, 2, 16, JW>);
+  else
+    switch (score_rows(kv.G)) {
+      case 1: return join(k_kv_join<D, T, 1, 1, JW>);
+      case 2: return join(k_kv_join<D, T, 1, 2, JW>);
+      case 4: return join(k_kv_join<D, T, 1, 4, JW>);
+      default: return join(k_kv_join<D, T, 1, 8, JW>);
+    }
 }
 
 template <int D, bool E4M3>

@@ -15,7 +15,8 @@
 // Bound by latency, then memory: mass and position are read once (8 bytes an
 // entry) into registers, with every load in flight before the first is used, and the
 // passes of the selection run on registers; then the moved rows are read and
-// written.  A cluster of blocks shares one (sequence, KV head) while there are few of
+// written (a ragged half of 32 sequences, 8 KV heads: 16 us of selection, 31 us for 160 MB of
+// moves, 5.2 TB/s).  A cluster of blocks shares one (sequence, KV head) while there are few of
 // them; histograms and counts meet over distributed shared memory, every block
 // reading the others', so that a pass waits for the cluster once.
 #include <cooperative_groups.h>
@@ -481,10 +482,12 @@ cudaError_t launch_kv_evict(const KvEvictArgs& args, int row_bytes, int device, 
   a.rows = (int64_t)kv.n_pages * kv.Hkv << kv.page_shift;
   carve(a.w, args.work, kv.n_seqs, kv.Hkv, a.rows);
   a.items = kv.n_seqs * kv.Hkv;
-  // Blocks of a cluster: one takes 2,048 entries in 4 a thread; more share longer
-  // sequences while the items alone do not fill the GPU.
+  // Blocks of a cluster: one takes 4,096 entries in 8 a thread; more share longer sequences
+  // while the items alone do not fill the GPU.  A pass costs a cluster 1.7 to 3 us, one block
+  // alone 1.2 (64 items of 2,112 entries: 12.9 us alone, 15.4 in pairs), and what a thread
+  // reads beyond that costs more (two sequences of 131,000: 42 us in 16 blocks, 89 in 8).
   int blocks = 1;
-  while (blocks < 16 && kv.cap > 2048 * blocks && a.items * blocks * 2 <= sms) blocks *= 2;
+  while (blocks < 16 && kv.cap > 4096 * blocks && a.items * blocks * 2 <= sms) blocks *= 2;
   // Entries of a thread, by the longest sequence the table has room for: all of them in
   // registers where they are 32 at most.
   const int share = (kv.cap + blocks - 1) / blocks, each = (share + kSelThreads - 1) / kSelThreads;

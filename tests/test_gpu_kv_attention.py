@@ -60,7 +60,8 @@ MIXED = [0, 1, 2, 15, 16, 17, 0, 33, 100, 257, 1000, 0]
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("dim,heads,kv_heads,page", [
     (64, 4, 4, 16), (64, 24, 1, 64), (96, 6, 2, 32), (96, 33, 3, 8), (128, 16, 2, 16), (128, 15, 3, 8),
-    (128, 40, 1, 128), (192, 9, 1, 16), (192, 32, 2, 8), (256, 16, 2, 64), (256, 12, 1, 16), (256, 64, 4, 1024)])
+    (128, 40, 1, 128), (192, 9, 1, 16), (192, 32, 2, 8), (256, 16, 2, 64), (256, 12, 1, 16), (256, 64, 4, 1024),
+    (64, 12, 3, 16), (128, 6, 3, 32), (256, 3, 3, 16), (96, 9, 3, 16)])
 def test_mixed_lengths(dim, heads, kv_heads, page, e4m3):
     c = Cache(MIXED, heads, kv_heads, dim, page, e4m3, seed=dim + heads)
     check(c, MIXED, queries(c, len(MIXED)), dim ** -0.5, mass=True)
