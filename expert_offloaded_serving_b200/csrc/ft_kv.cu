@@ -40,6 +40,8 @@ ft_status check_shape(const ft_kv_cache* c) {
   if (c->n_kv_heads <= 0 || c->n_heads <= 0 || c->n_heads % c->n_kv_heads || c->n_heads > 65536)
     return refuse(FT_ERR_INVALID, "n_heads %d is not a positive multiple of n_kv_heads %d, at most 65536", c->n_heads,
                   c->n_kv_heads);
+  if (c->n_heads / c->n_kv_heads > 1024)
+    return refuse(FT_ERR_INVALID, "n_heads / n_kv_heads %d is above 1024", c->n_heads / c->n_kv_heads);
   if (c->page_size < 8 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
     return refuse(FT_ERR_INVALID, "page_size %d is not a power of two from 8 to 1024", c->page_size);
   if (c->n_seqs < 0 || c->n_seqs > ft::kKvMaxSeqs)
@@ -49,9 +51,9 @@ ft_status check_shape(const ft_kv_cache* c) {
   const int64_t rows_a_page = (int64_t)c->n_kv_heads * c->page_size;
   if (c->n_pages < 1 || c->n_pages >= ((int64_t)1 << 31) / rows_a_page)
     return refuse(FT_ERR_INVALID, "n_pages %lld: the pools hold 1 page to 2^31 - 1 rows", (long long)c->n_pages);
-  const int64_t groups = (c->n_heads / c->n_kv_heads + 15) / 16, tiles = ((int64_t)c->max_pages * c->page_size + 15) / 16;
-  if ((double)c->n_seqs * (double)tiles * (double)(c->n_kv_heads * groups) >= 1073741824.0)
-    return refuse(FT_ERR_INVALID, "n_seqs x max_pages x heads is too large: below 2^30 tiles of 16 entries");
+  const int64_t tiles = ((int64_t)c->max_pages * c->page_size + 15) / 16;
+  if ((double)c->n_seqs * (double)tiles * (double)c->n_kv_heads >= 1073741824.0)
+    return refuse(FT_ERR_INVALID, "n_seqs x max_pages x n_kv_heads is too large: below 2^30 tiles of 16 entries");
   if (c->format != FT_KV_BF16 && c->format != FT_KV_E4M3)
     return refuse(FT_ERR_INVALID, "format %d is not FT_KV_BF16 or FT_KV_E4M3", c->format);
   if (!(c->k_scale > 0) || !(c->v_scale > 0) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))

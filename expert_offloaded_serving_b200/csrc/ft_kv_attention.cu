@@ -16,10 +16,13 @@
 // loads: a tile of keys or values is one TMA copy into the ring of the warp that
 // uses it.
 //
-// Split: the unit is a tile of 16 or 32 entries of one (sequence, KV head, group of
-// 16 query heads).  All tiles of the batch, in that order, are cut into equal
-// contiguous chunks, one a warp; a warp streams its chunk through its own ring and
-// meets no barrier with other warps.  A row (the tiles of one item) that lies inside one
+// Split: the unit is a tile of 16 or 32 entries of one (sequence, KV head).  All tiles
+// of the batch, in that order, are cut into equal contiguous chunks, one a warp; a warp
+// streams its chunk through its own ring and meets no barrier with other warps.  With more
+// than 16 query heads a KV head, a chunk goes to one warp for each group of 16: they
+// begin together, so memory is read once and L2 serves the rest (32 sequences of 16,000 entries, 32
+// heads over one of 128: 71 us, 75 with the groups one after the other).  A row (the tiles of one
+// KV head) that lies inside one
 // chunk is finished there; the parts of the others go to the workspace (fp32) and
 // k_kv_join adds them in the order of the chunks.  Lengths are read on the device:
 // ragged batches and idle rows are balanced by construction, a captured graph stays
@@ -42,7 +45,7 @@ namespace ft {
 
 namespace {
 
-constexpr int kRows = 16;        // query heads of an item: rows of the mma tile
+constexpr int kRows = 16;        // query heads of a group, which one warp takes
 
 // The ring of a warp for entries of RB bytes a side: a stage holds a tile of keys
 // and one of values as TMA leaves them, boxes of kBox bytes x the tile's rows whose
@@ -71,47 +74,50 @@ struct Ring {
 };
 
 
-// What chunk j leaves for block j of k_kv_join.
+// What warp j leaves for block j of k_kv_join: chunk j / groups, for the query heads of group j % groups.
 struct __align__(16) Chunk {
-  int b, hh, first, len;  // sequence and item of its first tile, that row's first tile in the batch and its entries
+  int b, h, first, len;   // sequence and KV head of its first tile, that row's first tile in the batch and its entries
   int tiles, size;        // its tiles (0: none), tiles of a chunk in this launch
-  int go_b, go_hh;        // the row that goes on past its end (go_b -1: none)
+  int go_b, go_h;         // the row that goes on past its end (go_b -1: none)
   int go_j0, go_parts;    // the chunk that row begins on, the chunks it lies on
   int pad[2];
 };
 struct AttnWork {
   Chunk* chunks;
-  float2* ml;        // [chunks][2][8 or 16] m and l of a part (log2 units); side 0: a row that came in, 1: one that goes on
-  float* o;          // [chunks][2][8 or 16][D]
+  float2* ml;        // [warps][2][8 or 16] m and l of a part (log2 units); side 0: a row that came in, 1: one that goes on
+  float* o;          // [warps][2][8 or 16][D]
   float* lse2;       // [n_seqs][Hq] lse of whole rows in log2 units (mass)
-  float* scores;     // [tiles][entries of a tile][score_rows] scores in log2 units (mass)
+  float* scores;     // [groups][tiles][entries of a tile][score_rows] scores in log2 units (mass)
   int64_t tiles;     // that `scores` holds
 };
 
 __host__ __device__ inline int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
-// Scores kept of an entry, for G query heads a KV head: as many of the 8 or 16 rows of an item as a power of two covers.
+// Scores kept of an entry, for G query heads a KV head: as many of the 8 or 16 heads of a warp as a power of two covers.
 __host__ __device__ inline int score_rows(int G) { return G > 8 ? 16 : G > 4 ? 8 : G > 2 ? 4 : G; }
+
+// Query heads of a KV head go in groups of 16.
+__host__ __device__ inline int groups_of(int G) { return (G + kRows - 1) / kRows; }
 
 // Scores of the tiles that sequences of their own pages can have: every row of the pool, and a last tile each.
 inline int64_t carve(AttnWork& w, uint8_t* base, int D, int row_bytes, int n_seqs, int Hq, int Hkv, int64_t rows, bool mass) {
-  const int G = Hq / Hkv, tile = tile_of(row_bytes), kept = G > 8 ? 16 : 8;  // rows of an item
-  const int64_t chunks = kKvMaxSms * warps_of(row_bytes);
+  const int G = Hq / Hkv, tile = tile_of(row_bytes), kept = G > 8 ? 16 : 8;  // heads of a warp
+  const int64_t warps = kKvMaxSms * warps_of(row_bytes);
   int64_t at = 0;
   w.chunks = reinterpret_cast<Chunk*>(base + at);
-  at += up256(chunks * (int64_t)sizeof(Chunk));
+  at += up256(warps * (int64_t)sizeof(Chunk));
   w.ml = reinterpret_cast<float2*>(base + at);
-  at += up256(chunks * 2 * kept * (int64_t)sizeof(float2));
+  at += up256(warps * 2 * kept * (int64_t)sizeof(float2));
   w.o = reinterpret_cast<float*>(base + at);
-  at += up256(chunks * 2 * kept * D * (int64_t)sizeof(float));
+  at += up256(warps * 2 * kept * D * (int64_t)sizeof(float));
   w.lse2 = reinterpret_cast<float*>(base + at);
   w.scores = nullptr;
   w.tiles = 0;
   if (!mass) return at;
   at += up256((int64_t)n_seqs * Hq * sizeof(float));
   w.scores = reinterpret_cast<float*>(base + at);
-  w.tiles = (rows / tile + (int64_t)n_seqs * Hkv) * ((G + kRows - 1) / kRows);
-  at += up256(w.tiles * tile * score_rows(G) * (int64_t)sizeof(float));
+  w.tiles = rows / tile + (int64_t)n_seqs * Hkv;
+  at += up256(w.tiles * groups_of(G) * tile * score_rows(G) * (int64_t)sizeof(float));
   return at;
 }
 
@@ -119,8 +125,8 @@ struct SplitArgs {
   CUtensorMap k_map, v_map;  // pools as kBox bytes x rows x kBoxes; a box has box_rows, and all kBoxes where that is a tile's rows
   KvAttnArgs a;
   AttnWork w;
-  int groups;     // items of a KV head: groups of 16 query heads
-  float per_warp;  // 1 / warps of the launch
+  int groups;      // of 16 query heads, a KV head
+  float per_chunk;  // 1 / chunks of the launch
   float per_part;  // 1 / (rows x kMaxParts)
   int box_shift;  // box_rows = 1 << box_shift: a tile's rows, or a page's where pages are smaller
 };
@@ -204,9 +210,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// A place in the batch's order of tiles: sequence, item of the sequence, tile of the item.
+// A place in the batch's order of tiles: sequence, KV head, tile of the row.
 struct Place {
-  int b, hh, t, len, nt;
+  int b, h, t, len, nt;
 };
 
 template <int TILE>
@@ -224,11 +230,11 @@ __device__ __forceinline__ void next_sequence(const KvView& kv, Place& p) {
 }
 
 template <int TILE>
-__device__ __forceinline__ void advance(const KvView& kv, Place& p, int items) {
+__device__ __forceinline__ void advance(const KvView& kv, Place& p) {
   if (++p.t < p.nt) return;
   p.t = 0;
-  if (++p.hh < items) return;
-  p.hh = 0;
+  if (++p.h < kv.Hkv) return;
+  p.h = 0;
   next_sequence<TILE>(kv, p);
 }
 
@@ -246,8 +252,8 @@ constexpr int kMaxParts = 64;
 // within f16.
 constexpr float kSlack = 8.0f;
 
-// D: head_dim.  E4M3: the cache's format.  NB: blocks of 8 query heads of an
-// item.  MASS: scores go to the workspace.
+// D: head_dim.  E4M3: the cache's format.  NB: blocks of 8 query heads of a
+// warp.  MASS: scores go to the workspace.
 template <int D, bool E4M3, int NB, bool MASS>
 __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv_split(const __grid_constant__ SplitArgs args) {
   constexpr int RB = D * (E4M3 ? 1 : 2);
@@ -265,7 +271,6 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
 
   const KvView& kv = args.a.kv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int items = kv.Hkv * args.groups;
 
   uint64_t* const full = s_full + warp * R::kStages;
   if (lane < R::kStages) tc::mbar_init(full + lane, 1);
@@ -277,12 +282,14 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
   kv_pdl_wait();
   kv_pdl_trigger();
   const int j = warp * gridDim.x + blockIdx.x;  // neighbours in the batch sit on different SMs
-  const int warps = (int)gridDim.x * R::kWarps;
-  auto chunk_of = [&](int total) {  // ceil(total / warps), exact: the estimate is at most one off
-    int n = (int)((float)total * args.per_warp);
-    n += n * warps < total;
-    n += n * warps < total;
-    n -= (n - 1) * warps >= total && n > 0;
+  const int groups = NB == 1 ? 1 : args.groups;
+  const int warps = (int)gridDim.x * R::kWarps, chunks = warps / groups;
+  const int c = j / groups, gi = j - c * groups;  // the warp's chunk and group; c can be `chunks`: nothing there
+  auto chunk_of = [&](int total) {  // ceil(total / chunks), exact: the estimate is at most one off
+    int n = (int)((float)total * args.per_chunk);
+    n += n * chunks < total;
+    n += n * chunks < total;
+    n -= (n - 1) * chunks >= total && n > 0;
     return max(max(n, 1), min(4, (int)((float)total * args.per_part)));
   };
   // The tiles of the batch are counted, cut, and the chunk's first one is looked up: its
@@ -291,7 +298,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
   int base, total, chunk, lo, hi;
   auto cut = [&] {
     chunk = chunk_of(total);
-    lo = (int)min((int64_t)j * chunk, (int64_t)total);
+    lo = (int)min((int64_t)c * chunk, (int64_t)total);
     hi = min(lo + chunk, total);
   };
   if (kv.n_seqs <= 128) {  // every warp by itself, four sequences a lane
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     for (int i = 0; i < 4; i++) {
       upto[i] = total;
       if (i * 32 >= kv.n_seqs) continue;
-      int run = tiles_of<TILE>(len[i]) * items;
+      int run = tiles_of<TILE>(len[i]) * kv.Hkv;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, run, d);
@@ -324,14 +331,14 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
       if (i * 32 >= kv.n_seqs || before == 32) continue;
       cons.b = i * 32 + before;
       cons.len = __shfl_sync(0xffffffffu, len[i], before);
-      base = __shfl_sync(0xffffffffu, upto[i], before) - tiles_of<TILE>(cons.len) * items;
+      base = __shfl_sync(0xffffffffu, upto[i], before) - tiles_of<TILE>(cons.len) * kv.Hkv;
     }
   } else {  // the block together: a run of `per` sequences a thread
     const int per = (kv.n_seqs + kThreads - 1) / kThreads;
     int sum = 0;
     for (int i = 0; i < per; i++) {
       const int b = tid * per + i;
-      if (b < kv.n_seqs) sum += tiles_of<TILE>(kv_length(kv, b, blockIdx.x == 0)) * items;
+      if (b < kv.n_seqs) sum += tiles_of<TILE>(kv_length(kv, b, blockIdx.x == 0)) * kv.Hkv;
     }
     int run = sum;
 #pragma unroll
@@ -358,7 +365,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     cons.len = 0;
     for (; lo < hi && cons.b < kv.n_seqs; cons.b++) {
       cons.len = kv_length(kv, cons.b);
-      const int n = tiles_of<TILE>(cons.len) * items;
+      const int n = tiles_of<TILE>(cons.len) * kv.Hkv;
       if (lo < base + n) break;
       base += n;
     }
@@ -384,10 +391,10 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     return;
   }
   cons.nt = tiles_of<TILE>(cons.len);
-  cons.hh = (lo - base) / cons.nt;
-  cons.t = (lo - base) - cons.hh * cons.nt;
+  cons.h = (lo - base) / cons.nt;
+  cons.t = (lo - base) - cons.h * cons.nt;
   int row_first = lo - cons.t;  // first tile of the present row in the batch's order
-  Chunk left{cons.b, cons.hh, row_first, cons.len, hi - lo, chunk, -1, 0, 0, 0, {0, 0}};
+  Chunk left{cons.b, cons.h, row_first, cons.len, hi - lo, chunk, -1, 0, 0, 0, {0, 0}};
 
   uint8_t* const ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u) + warp * (R::kStages * R::kStage);
   const uint32_t ring32 = smem_u32(ring);
@@ -398,7 +405,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
   const int box_shift = args.box_shift, box_bytes = RB << box_shift;
   auto box_row = [&](const Place& p) {  // first row of the lane's box, -1 where there is none
     const int slot = p.t * TILE + (lane << box_shift);
-    return lane < (TILE >> box_shift) && slot < p.len ? kv_row(kv, p.b, p.hh / args.groups, slot) : -1;
+    return lane < (TILE >> box_shift) && slot < p.len ? kv_row(kv, p.b, p.h, slot) : -1;
   };
   int row_next = box_row(prod), left_next = prod.len - prod.t * TILE;
   int to_load = hi - lo;
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     to_load--;
     const int row = row_next, left = left_next;
     if (to_load > 0) {
-      advance<TILE>(kv, prod, items);
+      advance<TILE>(kv, prod);
       row_next = box_row(prod);
       left_next = prod.len - prod.t * TILE;
     }
@@ -438,12 +445,11 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
   uint32_t q[D / 16][NB][2];
   float o[D / 16][NB][4];
   float m[NB][2], l[NB][2], qs[NB][2];
-  int n_rows = 0, head0 = 0;
+  const int n_rows = min(kRows, kv.G - gi * kRows);
+  int head0 = 0;
 
-  auto begin_row = [&](int b, int hh) {
-    const int h = hh / args.groups, gi = hh - h * args.groups;
+  auto begin_row = [&](int b, int h) {
     head0 = h * kv.G + gi * kRows;
-    n_rows = min(kRows, kv.G - gi * kRows);
     const float unit = args.a.scale * 1.4426950408889634f * kv.k_scale;
 #pragma unroll
     for (int nb = 0; nb < NB; nb++) {
@@ -567,7 +573,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
   uint32_t phase = 0;
   bool broken = false;
   bool fresh = true;  // a row begins with this tile
-  begin_row(cons.b, cons.hh);  // q is on its way before the tiles fill the memory's queues
+  begin_row(cons.b, cons.h);  // q is on its way before the tiles fill the memory's queues
 #pragma unroll 1
   for (int s = 0; s < R::kStages - 1; s++) load(s);
 #pragma unroll 1
@@ -668,7 +674,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
       }
     if (MASS && at < args.w.tiles) {
       const int kept = NB == 2 ? 16 : score_rows(kv.G);  // of an entry
-      float* sc = args.w.scores + ((int64_t)at * TILE + g) * kept + j2;
+      float* sc = args.w.scores + ((gi * args.w.tiles + at) * TILE + g) * kept + j2;
 #pragma unroll
       for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -767,14 +773,14 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
       end_row(cons.b, last && row_first >= lo, row_first >= lo ? 1 : 0);
       if (!last) {
         left.go_b = cons.b;
-        left.go_hh = cons.hh;
+        left.go_h = cons.h;
         left.go_j0 = row_first / chunk;
         left.go_parts = (row_first + cons.nt - 1) / chunk - left.go_j0 + 1;
       }
       row_first += cons.nt;
       if (at + 1 < hi) {
-        advance<TILE>(kv, cons, items);
-        begin_row(cons.b, cons.hh);
+        advance<TILE>(kv, cons);
+        begin_row(cons.b, cons.h);
       }
       fresh = true;
     } else {
@@ -799,13 +805,13 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
 }
 
 // ---------------------------------------------------------------------------
-// join: block j serves the row that goes on past the end of chunk j.  The P
-// parts of a row lie on the chunks j0 .. j0+P-1, so P - 1 blocks share it: a row
-// in many parts has many blocks.  Part p lies on chunk j0 + p, side 1 (the row
-// begins) for p = 0, else side 0.
+// join: block j serves the row that goes on past the end of warp j's chunk, for that
+// warp's group of heads.  The P parts of a row lie on the chunks j0 .. j0+P-1, so P - 1
+// blocks of a group share it: a row in many parts has many blocks.  Part p lies on chunk
+// j0 + p, side 1 (the row begins) for p = 0, else side 0.
 //
-// With MASS it then adds the weights of chunk j's entries: 2^(score - lse)
-// over the query heads of their KV head.  Every warp of both goes its own way: one
+// With MASS the blocks of a chunk, one for each group, then add the weights of its
+// entries: 2^(score - lse) over the query heads of their KV head.  Every warp of both goes its own way: one
 // trip to memory for what it joins.
 // ---------------------------------------------------------------------------
 struct JoinArgs {
@@ -826,10 +832,11 @@ template <int D, int NB, int WARPS>
 __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
   const KvView& kv = args.a.kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = c.go_hh / args.groups, gi = c.go_hh - h * args.groups;
+  const int groups = NB == 1 ? 1 : args.groups;
+  const int at = (int)blockIdx.x / groups, gi = (int)blockIdx.x - at * groups;
   const int n_rows = min(kRows, kv.G - gi * kRows);
-  const int64_t head0 = (int64_t)c.go_b * kv.Hq + h * kv.G + gi * kRows;
-  const int parts = c.go_parts, blocks = parts - 1, mine = (int)blockIdx.x - c.go_j0;
+  const int64_t head0 = (int64_t)c.go_b * kv.Hq + c.go_h * kv.G + gi * kRows;
+  const int parts = c.go_parts, blocks = parts - 1, mine = at - c.go_j0;
   // Units of four dims of a row.  `split` lanes share a unit's parts while
   // there are more threads than units.
   const int units = n_rows * (D / 4), threads = blocks * WARPS * 32;
@@ -851,7 +858,7 @@ __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
     };
 #pragma unroll 8
     for (int p = lane / width; p < parts; p += split) {
-      const int64_t at = ((int64_t)(c.go_j0 + p) * 2 + (p == 0 ? 1 : 0)) * (8 * NB) + row;
+      const int64_t at = (((int64_t)(c.go_j0 + p) * groups + gi) * 2 + (p == 0 ? 1 : 0)) * (8 * NB) + row;
       const float2 ml = args.w.ml[at];
       add(ml.x, ml.y, *reinterpret_cast<const float4*>(args.w.o + at * D + d4 * 4));
     }
@@ -885,7 +892,7 @@ struct Floats<4> {
   using type = float4;
 };
 
-// The warp's share of a chunk's tiles.  L lanes hold an entry's KEPT scores, V query heads
+// The warp's share of a chunk's tiles, cut over the warps of all blocks of the chunk.  L lanes hold an entry's KEPT scores, V query heads
 // each; 32 / L entries go at a time, and after L of them each lane has the sum
 // of one entry.
 template <int TILE, int KEPT, int WARPS>
@@ -899,19 +906,19 @@ __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
   };
   const KvView& kv = args.a.kv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L, set = lane / L;
-  const int items = kv.Hkv * args.groups, share = (c.tiles + WARPS - 1) / WARPS;
-  const int chunk0 = (int)blockIdx.x * c.size, lo = chunk0 + min(c.tiles, warp * share), hi = min(chunk0 + c.tiles, lo + share);
-  Place p{c.b, c.hh, 0, c.len, tiles_of<TILE>(c.len)};
+  const int groups = KEPT < 16 ? 1 : args.groups;
+  const int here = (int)blockIdx.x / groups, turn = ((int)blockIdx.x - here * groups) * WARPS + warp;
+  const int share = (c.tiles + WARPS * groups - 1) / (WARPS * groups);
+  const int chunk0 = here * c.size, lo = chunk0 + min(c.tiles, turn * share), hi = min(chunk0 + c.tiles, lo + share);
+  if (lo >= hi) return;
+  Place p{c.b, c.h, 0, c.len, tiles_of<TILE>(c.len)};
   for (int first = c.first; first < hi;) {
-    const int h = p.hh / args.groups;
-    // the first group's tiles stand for the entries; all groups are added there
-    const bool counts = p.hh == h * args.groups && first + p.nt > lo;
+    const int j0 = first / c.size, parts = (first + p.nt - 1) / c.size - j0 + 1;
     const int e0 = (max(lo, first) - first) * TILE, e1 = min((min(hi, first + p.nt) - first) * TILE, p.len);
-    for (int gi = 0; counts && gi < args.groups; gi++) {
-      const int row_first = first + gi * p.nt, j0 = row_first / c.size;
-      const int parts = (row_first + p.nt - 1) / c.size - j0 + 1, n_rows = min(kRows, kv.G - gi * kRows);
-      const float* const scores = args.w.scores + (int64_t)row_first * TILE * KEPT + sub * V;
-      const int last = (int)min((int64_t)e1, (args.w.tiles - row_first) * TILE);  // entries whose scores were kept
+    const int last = (int)min((int64_t)e1, (args.w.tiles - first) * TILE);  // entries whose scores were kept
+    for (int gi = 0; first + p.nt > lo && gi < groups; gi++) {
+      const int n_rows = min(kRows, kv.G - gi * kRows);
+      const float* const scores = args.w.scores + (gi * args.w.tiles + first) * TILE * KEPT + sub * V;
       Scores x[RUNS][L];
       int row[RUNS];
       auto load = [&](int e) {  // the lane keeps the sum of entry sub * E + set of each run
@@ -927,7 +934,7 @@ __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
 #pragma unroll
         for (int r = 0; r < RUNS; r++) {
           const int own = e + 32 * r + sub * E + set;
-          row[r] = own < last ? kv_row(kv, p.b, h, own) : -1;
+          row[r] = own < last ? kv_row(kv, p.b, p.h, own) : -1;
         }
       };
       if (e0 < last) load(e0);
@@ -935,10 +942,10 @@ __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
       if (parts == 1) {
 #pragma unroll
         for (int i = 0; i < V; i++)
-          z[i] = sub * V + i < n_rows ? args.w.lse2[(int64_t)p.b * kv.Hq + h * kv.G + gi * kRows + sub * V + i] : kNegInf;
+          z[i] = sub * V + i < n_rows ? args.w.lse2[(int64_t)p.b * kv.Hq + p.h * kv.G + gi * kRows + sub * V + i] : kNegInf;
       } else {
         auto part = [&](int q, float2 (&ml)[V]) {
-          const float2* at = args.w.ml + ((int64_t)(j0 + q) * 2 + (q == 0 ? 1 : 0)) * ROWS + sub * V;
+          const float2* at = args.w.ml + (((int64_t)(j0 + q) * groups + gi) * 2 + (q == 0 ? 1 : 0)) * ROWS + sub * V;
           if constexpr (V == 4) {
             const float4 u = reinterpret_cast<const float4*>(at)[0], v = reinterpret_cast<const float4*>(at)[1];
             ml[0] = make_float2(u.x, u.y), ml[1] = make_float2(u.z, u.w);
@@ -1004,7 +1011,7 @@ __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
     first += p.nt;
     if (first < hi) {
       p.t = p.nt - 1;
-      advance<TILE>(kv, p, items);
+      advance<TILE>(kv, p);
     }
   }
 }
@@ -1029,8 +1036,8 @@ cudaError_t run(SplitArgs& a, int device, int sms, cudaStream_t s) {
   const uint64_t rows = (uint64_t)kv.n_pages * kv.Hkv << kv.page_shift;
   a.box_shift = R::kTile == 32 ? 5 : 4;
   if (kv.page_shift < a.box_shift) a.box_shift = kv.page_shift;
-  a.per_warp = 1.0f / (float)(sms * R::kWarps);
-  a.per_part = 1.0f / ((float)kv.n_seqs * (float)(kv.Hkv * a.groups) * kMaxParts);
+  a.per_chunk = 1.0f / (float)(sms * R::kWarps / a.groups);
+  a.per_part = 1.0f / ((float)kv.n_seqs * (float)kv.Hkv * kMaxParts);
   const uint32_t deep = (1 << a.box_shift) == R::kTile ? R::kBoxes : 1;
   if (encode_tmap_rows(&a.k_map, kv.k, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift, deep) != FT_OK ||
       encode_tmap_rows(&a.v_map, kv.v, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift, deep) != FT_OK)
@@ -1072,7 +1079,7 @@ int64_t kv_attn_workspace(const ft_kv_cache& c) {
 cudaError_t launch_kv_attention(const KvAttnArgs& args, bool e4m3, int device, int sms, cudaStream_t s) {
   SplitArgs a;
   a.a = args;
-  a.groups = (args.kv.G + kRows - 1) / kRows;
+  a.groups = groups_of(args.kv.G);
   const KvView& kv = args.kv;
   carve(a.w, args.work, kv.D, kv.D * (e4m3 ? 1 : 2), kv.n_seqs, kv.Hq, kv.Hkv,
         (int64_t)kv.n_pages * kv.Hkv << kv.page_shift, args.mass);

@@ -561,12 +561,12 @@ FT_API ft_status ft_moe_layer_forward_noalloc(int32_t hidden, int32_t inter, int
  * or the entry (bad page) and accesses nothing out of bounds. */
 typedef struct {
   int32_t head_dim;      /* D: 64, 96, 128, 192 or 256 */
-  int32_t n_heads;       /* query heads, a multiple of n_kv_heads; the heads h*G .. h*G+G-1 share KV head h */
+  int32_t n_heads;       /* query heads, a multiple of n_kv_heads; the heads h*G .. h*G+G-1 share KV head h (G <= 1024) */
   int32_t n_kv_heads;
   int32_t page_size;     /* entries of a page: a power of two from 8 to 1024 */
   int32_t n_seqs;        /* rows of block_table and lengths, at most 65536 (0: every call is a no-op) */
   int32_t max_pages;     /* columns of block_table; max_pages * page_size <= 2^30, and n_seqs * n_kv_heads
-                            times its 16ths (and times the 16ths of n_heads/n_kv_heads) below 2^30 */
+                            times its 16ths below 2^30 */
   int64_t n_pages;       /* pages of the pools; n_pages * n_kv_heads * page_size < 2^31 */
   int32_t format;        /* FT_KV_BF16 or FT_KV_E4M3 */
   float k_scale;         /* what one unit of a stored key / value stands for (E4M3: positive and finite; */

@@ -75,6 +75,14 @@ def test_few_rows_split_over_the_gpu(lengths, e4m3):
     check(c, lengths, queries(c, len(lengths)), 128 ** -0.5, mass=True)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,lengths", [(17, 1, [5000, 3, 0, 700]), (96, 3, [4001, 1, 2222]), (128, 2, [9000]),
+                                                    (1024, 1, [1, 40, 333]), (1000, 2, [129])])
+def test_groups_of_heads_over_rows_in_many_parts(heads, kv_heads, lengths, e4m3):
+    c = Cache(lengths, heads, kv_heads, 64, 16, e4m3, seed=heads)
+    check(c, lengths, queries(c, len(lengths)), 0.125, mass=True)
+
+
 @pytest.mark.parametrize("n_seqs", [32, 33, 128, 129, 257])
 def test_counts_of_sequences_around_the_ways_to_find_a_place(n_seqs):
     lengths = [0 if i % 5 == 3 else (i * 977) % 301 for i in range(n_seqs)]

@@ -68,6 +68,14 @@ def test_every_call_refuses_a_bad_shape(kw, what):
     assert n.value == -7
 
 
+def test_every_call_refuses_more_than_1024_query_heads_a_kv_head():
+    kv = cache(n_heads=1025, n_kv_heads=1)
+    for call in (append, attend, evict):
+        refused(call(kv), "above 1024")
+    refused(ft.lib().ft_kv_workspace_bytes(C.byref(kv), C.byref(ft.I64())), "above 1024")
+    assert ft.ft_kv_workspace_bytes(cache(n_heads=1024, n_kv_heads=1)) > 0
+
+
 @pytest.mark.parametrize("kw,what", [
     (dict(k=None), "NULL"), (dict(v=None), "NULL"), (dict(block_table=None), "NULL"), (dict(lengths=None), "NULL"),
     (dict(k=K + 8), "16-byte"), (dict(v=V + 2), "16-byte"), (dict(mass=MASS + 2), "4-byte"), (dict(pos=POS + 1), "4-byte"),
