@@ -56,9 +56,11 @@ constexpr int kRows = 16;        // query heads of a group, which one warp takes
 // products, up to rows of 256 bytes (131,072 entries of 256 bytes 93 us, 16 entries a tile 96).
 // There 4 warps x 3 stages match 6 x 2 on long rows (93 and 92 us) and win on 64 sequences of 200
 // entries (12.4 against 15.3); rows of 128 bytes want 8 warps (a ragged batch 56.8 us, 59.7 with
-// 6); beyond 256 the registers of O leave room for 4.
+// 6; 16 x 8,000 entries and 64 heads over 4: 34.2, 36.1 with 12), rows of 96 too (16 heads over one: 29.6,
+// 33.1 with 12), rows of 64 want 16 (16 x 8,000 entries, 8 heads: 30.7, 33.4 with 8); beyond 256
+// the registers of O leave room for 4.
 constexpr int tile_of(int row_bytes) { return row_bytes <= 256 ? 32 : 16; }
-constexpr int warps_of(int row_bytes) { return row_bytes >= 256 ? 4 : 8; }
+constexpr int warps_of(int row_bytes) { return row_bytes >= 256 ? 4 : row_bytes == 64 ? 16 : 8; }
 template <int RB>
 struct Ring {
   static constexpr int kTile = tile_of(RB);  // entries
