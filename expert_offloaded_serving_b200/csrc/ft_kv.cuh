@@ -42,7 +42,7 @@ __device__ __forceinline__ int kv_length(const KvView& kv, int b, bool tell = fa
 // Row of entry `slot` of sequence b and KV head h, or -1 (and the status)
 // where the table names no page of the pool.
 __device__ __forceinline__ int kv_row(const KvView& kv, int b, int h, int slot) {
-  const int page = __ldg(kv.table + (int64_t)b * kv.max_pages + (slot >> kv.page_shift));
+  const int page = kv.table[(int64_t)b * kv.max_pages + (slot >> kv.page_shift)];
   if ((unsigned)page >= (unsigned)kv.n_pages) {
     set_status(kv.status, kStBadId);
     return -1;
@@ -107,7 +107,9 @@ inline cudaError_t kv_attribute_once(std::atomic<uint64_t>& done, int device, F*
 // Launch with programmatic stream serialisation: the kernel may start while
 // its predecessor on the stream still runs.  Every thread of every kernel here executes
 // griddepcontrol.wait before it touches memory that another kernel may have
-// written or still reads, so a grid ends only after all those before it.
+// written or still reads, so a grid ends only after all those before it.  Loads are plain
+// ones for the same reason: one that is marked read-only for the whole kernel may be moved
+// to before the wait.
 template <typename A>
 inline cudaError_t kv_launch_after(void (*kern)(const A), dim3 grid, int threads, size_t smem, cudaStream_t s, const A& a) {
   cudaLaunchConfig_t cfg{};

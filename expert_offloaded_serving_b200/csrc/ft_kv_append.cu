@@ -29,7 +29,7 @@ struct Vec8 {
 };
 
 __device__ __forceinline__ Vec8 load8(const uint16_t* p) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
   Vec8 r;
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kThreads, 6) k_kv_append(KvAppendArgs a, int g
   int ax = -1;
   double freq = 0.0;
   if (u < rows) {
-    ax = __ldg(a.axis + f);
-    freq = __ldg(a.inv_freq + f);
+    ax = a.axis[f];
+    freq = a.inv_freq[f];
     if ((unsigned)ax >= (unsigned)a.n_axes) ax = -1;
   }
 
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 6) k_kv_append(KvAppendArgs a, int g
     const int32_t* const at = a.positions + (int64_t)max(ax, 0) * a.T + t0;
 #pragma unroll 1
     for (int tt = u; tt < nt; tt += rows) {
-      const int p = ax >= 0 ? __ldg(at + tt) : -1;
+      const int p = ax >= 0 ? at[tt] : -1;
       if (p < 0) s_bad[tt] = 1;
       const double turn = (double)p * freq;
       const double rest = fma(rint(turn * 0.15915494309189533577), -6.2831853071795864769, turn);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 6) k_kv_append(KvAppendArgs a, int g
     const int row = find_row(a, t0, nt), mine = tid - (kThreads - 32);
     if (mine < nt) {
       s_row[mine] = row;
-      if (a.positions && __ldg(a.positions + t0 + mine) < 0) s_bad[mine] = 1;
+      if (a.positions && a.positions[t0 + mine] < 0) s_bad[mine] = 1;
     }
   }
   __syncthreads();
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 6) k_kv_append(KvAppendArgs a, int g
     const int at = w.piece * 8, row = row0 + (w.head << kv.page_shift);
     const uint16_t* src = s_src[w.token][2] + w.head * D + at;
     if (E4M3) store8_e4m3(kv.v + (int64_t)row * D + at, load8(src), v_inv);
-    else *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(kv.v) + (int64_t)row * D + at) = __ldg(reinterpret_cast<const uint4*>(src));
+    else *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(kv.v) + (int64_t)row * D + at) = *reinterpret_cast<const uint4*>(src);
   }
   if (blockIdx.y == 0) {
     if (tid < nt && s_row[tid] >= 0 && s_bad[tid]) set_status(kv.status, kStBadId);
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 6) k_kv_append(KvAppendArgs a, int g
       if (row0 < 0) continue;
       const int row = row0 + ((i - token * kv.Hkv) << kv.page_shift);
       if (kv.mass) kv.mass[row] = 0.0f;
-      if (kv.pos) kv.pos[row] = __ldg(a.positions + t0 + token);
+      if (kv.pos) kv.pos[row] = a.positions[t0 + token];
     }
   }
 }

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kSelThreads, ONE && N <= 16 ? 2 : 1) k_kv_sele
 #pragma unroll
     for (int e = 0; e < N; e++) {
       const int i = i0 + 32 * e + lane;
-      row[e] = i < w_end ? __ldg(pages + (i >> kv.page_shift)) : 0;
+      row[e] = i < w_end ? pages[i >> kv.page_shift] : 0;
     }
 #pragma unroll
     for (int e = 0; e < N; e++) {
