@@ -22,9 +22,8 @@
 // than 16 query heads a KV head, a chunk goes to one warp for each group of 16: they
 // begin together, so memory is read once and L2 serves the rest (32 sequences of 16,000 entries, 32
 // heads over one of 128: 71 us, 75 with the groups one after the other).  A row (the tiles of one
-// KV head) that lies inside one
-// chunk is finished there; the parts of the others go to the workspace (fp32) and
-// k_kv_join adds them in the order of the chunks.  Lengths are read on the device:
+// KV head) that lies inside one chunk is finished there; the parts of the others go to the
+// workspace (fp32) and k_kv_join adds them in the order of the chunks.  Lengths are read on the device:
 // ragged batches and idle rows are balanced by construction, a captured graph stays
 // valid when lengths grow, and the split depends on nothing but the lengths and the
 // number of SMs.
@@ -34,9 +33,9 @@
 // is known.
 //
 // Measured (one B200, a graph of passes): 1 x 131,071 entries, 64 query and 8 KV heads of 128, BF16
-// 93 us (5.8 TB/s; the slowest SMs end at 86, the mean one at 77: the share of the
+// 92 us (5.8 TB/s; the slowest SMs end at 86, the mean one at 77: the share of the
 // memory's rate that an SM gets differs by 13 %); 64 sequences of 300 to 16,000 entries
-// 160 us (6.2 TB/s); 37 entries 7.5 us, two launches and four trips to memory.
+// 164 us (6 TB/s, 6.2 in the split); 37 entries 6.7 us, two launches and four trips to memory.
 #include "ft_gemm.h"
 #include "ft_kv.cuh"
 #include "ft_tc.cuh"

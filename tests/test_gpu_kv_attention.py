@@ -90,6 +90,14 @@ def test_counts_of_sequences_around_the_ways_to_find_a_place(n_seqs):
     check(c, lengths, queries(c, n_seqs), 0.125, mass=True)
 
 
+@pytest.mark.parametrize("heads", [2, 12])
+@pytest.mark.parametrize("n_seqs", [128, 129, 513, 1100])
+def test_counts_of_sequences_with_rows_of_64_bytes(n_seqs, heads):
+    lengths = [0 if i % 7 == 2 else (i * 977) % 97 for i in range(n_seqs)]
+    c = Cache(lengths, heads, 1, 64, 16, True, seed=n_seqs)
+    check(c, lengths, queries(c, n_seqs), 0.125, mass=True)
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_scores_of_a_hundred_million(e4m3):
     """Neighbouring fp32 scores are 16 apart there: a weight of 2^16 would not fit f16."""
