@@ -844,7 +844,9 @@ __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
   int split = 1;
   while (split < 32 && split * 2 <= parts && units * split * 2 <= threads) split *= 2;
   const int width = 32 / split;
-  for (int u0 = (mine * WARPS + warp) * width; u0 < units; u0 += blocks * WARPS * width) {
+  // Warps by block, then by turn: the first blocks to start share an SM, and a row of few units in many
+  // parts (100,000 E4M3 entries and one head of 128: 31 us, 17 so) would all be gathered by that one.
+  for (int u0 = (warp * blocks + mine) * width; u0 < units; u0 += blocks * WARPS * width) {
     const int u = min(u0 + lane % width, units - 1), row = u / (D / 4), d4 = u - row * (D / 4);
     float top = kNegInf, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
