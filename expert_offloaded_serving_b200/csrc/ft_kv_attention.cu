@@ -880,6 +880,13 @@ __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
   }
 }
 
+// A row in more parts than this has its lse found by the block together, not by each warp for itself:
+// 100,000 E4M3 entries and 16 heads of 128 34 us, 78 by warps alone; 11 ragged rows of up to 14,000
+// entries, 48 heads over two of 256 48.4 (from 32 parts on 49.8, from 64 on 54.8).  Few parts cost less by warps (13 rows
+// of up to 171 entries 18.4 us so, 19.6 with the block's way in the kernel at all).
+constexpr int kManyParts = 16;
+constexpr int kMaxGroups = 64;  // n_heads / n_kv_heads is at most 1024
+
 template <int V>
 struct Floats;
 template <>
@@ -895,9 +902,9 @@ struct Floats<4> {
   using type = float4;
 };
 
-// The warp's share of a chunk's tiles, cut over the warps of all blocks of the chunk.  L lanes hold an entry's KEPT scores, V query heads
-// each; 32 / L entries go at a time, and after L of them each lane has the sum
-// of one entry.
+// The warp's share of a chunk's tiles, cut over the warps of all blocks of the chunk.  L lanes
+// hold an entry's KEPT scores, V query heads each; 32 / L entries go at a time, and after L
+// of them each lane has the sum of one entry.
 template <int TILE, int KEPT, int WARPS>
 __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
   constexpr int ROWS = KEPT == 16 ? 16 : 8, V = KEPT < 4 ? KEPT : 4, L = KEPT / V, E = 32 / L;
@@ -913,6 +920,75 @@ __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
   const int here = (int)blockIdx.x / groups, turn = ((int)blockIdx.x - here * groups) * WARPS + warp;
   const int share = (c.tiles + WARPS * groups - 1) / (WARPS * groups);
   const int chunk0 = here * c.size, lo = chunk0 + min(c.tiles, turn * share), hi = min(chunk0 + c.tiles, lo + share);
+
+  // m and l of the lane's heads over the parts q, q + step, ... of a row, and over all lanes with these heads.
+  auto sum_parts = [&](int j0, int parts, int gi, int q, int step, float2 (&ml)[V]) {
+    auto part = [&](int q, float2 (&ml)[V]) {
+      const float2* at = args.w.ml + (((int64_t)(j0 + q) * groups + gi) * 2 + (q == 0 ? 1 : 0)) * ROWS + sub * V;
+      if constexpr (V == 4) {
+        const float4 u = reinterpret_cast<const float4*>(at)[0], v = reinterpret_cast<const float4*>(at)[1];
+        ml[0] = make_float2(u.x, u.y), ml[1] = make_float2(u.z, u.w);
+        ml[2] = make_float2(v.x, v.y), ml[3] = make_float2(v.z, v.w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) ml[i] = at[i];
+      }
+    };
+    part(min(q, parts - 1), ml);
+    if (q >= parts) {
+#pragma unroll
+      for (int i = 0; i < V; i++) ml[i].y = 0.0f;
+    }
+    for (q += step; q < parts; q += step) {
+      float2 y[V];
+      part(q, y);
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        const float both = fmaxf(ml[i].x, y[i].x);
+        ml[i].y = ml[i].y * rescale(ml[i].x, both) + y[i].y * rescale(y[i].x, both);
+        ml[i].x = both;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      float top = ml[i].x;
+#pragma unroll
+      for (int d = L; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      float sum = ml[i].y * rescale(ml[i].x, top);
+#pragma unroll
+      for (int d = L; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      ml[i] = make_float2(top, sum);
+    }
+  };
+  // Rows in many parts: the block's warps share them.  They can only be the chunk's first row and the one that goes on.
+  __shared__ float2 s_part[WARPS][ROWS];
+  __shared__ float s_lse[2][KEPT < 16 ? 1 : kMaxGroups][ROWS];
+  const int first_j0 = c.first / c.size, first_nt = tiles_of<TILE>(c.len);
+  const int first_parts = (c.first + first_nt - 1) / c.size - first_j0 + 1;
+  const bool other = c.go_b >= 0 && c.first + first_nt <= chunk0 + c.tiles;  // the row that goes on is not the first
+  for (int side = 0; side < 2; side++) {
+    const int j0 = side ? c.go_j0 : first_j0, parts = side ? (other ? c.go_parts : 0) : first_parts;
+    for (int gi = 0; parts > kManyParts && gi < groups; gi++) {
+      float2 ml[V];
+      sum_parts(j0, parts, gi, warp * E + set, WARPS * E, ml);
+      if (set == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i++) s_part[warp][sub * V + i] = ml[i];
+      }
+      __syncthreads();
+      if (threadIdx.x < KEPT) {
+        float top = kNegInf, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; w++) top = fmaxf(top, s_part[w][threadIdx.x].x);
+#pragma unroll
+        for (int w = 0; w < WARPS; w++) sum += s_part[w][threadIdx.x].y * rescale(s_part[w][threadIdx.x].x, top);
+        const bool real = threadIdx.x < kv.G - gi * kRows;
+        s_lse[side][gi][threadIdx.x] = real && sum != 0.0f ? top + __log2f(sum) : kNegInf;
+      }
+      __syncthreads();
+    }
+  }
+
   if (lo >= hi) return;
   Place p{c.b, c.h, 0, c.len, tiles_of<TILE>(c.len)};
   for (int first = c.first; first < hi;) {
@@ -946,44 +1022,14 @@ __device__ __forceinline__ void add_mass(const JoinArgs& args, const Chunk& c) {
 #pragma unroll
         for (int i = 0; i < V; i++)
           z[i] = sub * V + i < n_rows ? args.w.lse2[(int64_t)p.b * kv.Hq + p.h * kv.G + gi * kRows + sub * V + i] : kNegInf;
+      } else if (parts > kManyParts) {
+#pragma unroll
+        for (int i = 0; i < V; i++) z[i] = s_lse[first == c.first ? 0 : 1][gi][sub * V + i];
       } else {
-        auto part = [&](int q, float2 (&ml)[V]) {
-          const float2* at = args.w.ml + (((int64_t)(j0 + q) * groups + gi) * 2 + (q == 0 ? 1 : 0)) * ROWS + sub * V;
-          if constexpr (V == 4) {
-            const float4 u = reinterpret_cast<const float4*>(at)[0], v = reinterpret_cast<const float4*>(at)[1];
-            ml[0] = make_float2(u.x, u.y), ml[1] = make_float2(u.z, u.w);
-            ml[2] = make_float2(v.x, v.y), ml[3] = make_float2(v.z, v.w);
-          } else {
-#pragma unroll
-            for (int i = 0; i < V; i++) ml[i] = at[i];
-          }
-        };
         float2 ml[V];
-        part(min(set, parts - 1), ml);
-        if (set >= parts) {
+        sum_parts(j0, parts, gi, set, E, ml);
 #pragma unroll
-          for (int i = 0; i < V; i++) ml[i].y = 0.0f;
-        }
-        for (int q = set + E; q < parts; q += E) {
-          float2 y[V];
-          part(q, y);
-#pragma unroll
-          for (int i = 0; i < V; i++) {
-            const float both = fmaxf(ml[i].x, y[i].x);
-            ml[i].y = ml[i].y * rescale(ml[i].x, both) + y[i].y * rescale(y[i].x, both);
-            ml[i].x = both;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < V; i++) {
-          float top = ml[i].x;
-#pragma unroll
-          for (int d = L; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          float sum = ml[i].y * rescale(ml[i].x, top);
-#pragma unroll
-          for (int d = L; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-          z[i] = sub * V + i < n_rows && sum != 0.0f ? top + __log2f(sum) : kNegInf;
-        }
+        for (int i = 0; i < V; i++) z[i] = sub * V + i < n_rows && ml[i].y != 0.0f ? ml[i].x + __log2f(ml[i].y) : kNegInf;
       }
 #pragma unroll
       for (int i = 0; i < V; i++)

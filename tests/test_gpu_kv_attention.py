@@ -90,6 +90,14 @@ def test_counts_of_sequences_around_the_ways_to_find_a_place(n_seqs):
     check(c, lengths, queries(c, n_seqs), 0.125, mass=True)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("dim,heads", [(128, 1), (128, 2), (64, 3), (64, 12), (256, 20)])
+@pytest.mark.parametrize("lengths", [[40001], [9001, 9000, 5, 8000]])
+def test_weights_of_rows_in_many_parts(lengths, dim, heads, e4m3):
+    c = Cache(lengths, heads, 1, dim, 32, e4m3, seed=heads)
+    check(c, lengths, queries(c, len(lengths)), dim ** -0.5, mass=True)
+
+
 @pytest.mark.parametrize("heads", [2, 12])
 @pytest.mark.parametrize("n_seqs", [128, 129, 513, 1100])
 def test_counts_of_sequences_with_rows_of_64_bytes(n_seqs, heads):
