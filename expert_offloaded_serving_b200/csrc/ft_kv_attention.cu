@@ -593,13 +593,10 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     const uint32_t there = there_of[stage];
     if (there != kFull) {
       // Values that no sequence wrote could be NaN, which no weight of zero makes zero.
-#pragma unroll 1
-      for (int i = lane; i < TILE * kPieces; i += 32) {
-        const int e = i / kPieces, c = i - e * kPieces;
-        if (!((there >> e) & 1u))
-          *reinterpret_cast<uint4*>(ring + stage * R::kStage + R::kSide + (c / kBoxPieces) * R::kBoxBytes + e * R::kBox +
-                                    (c % kBoxPieces) * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
+      uint8_t* const v_box = ring + stage * R::kStage + R::kSide + lane * 16;
+#pragma unroll
+      for (int i = 0; i < TILE * kPieces / 32; i++)  // pieces in the order in which they lie: by box, entry, piece
+        if (!((there >> ((i * 32 + lane) / kBoxPieces % TILE)) & 1u)) *reinterpret_cast<uint4*>(v_box + i * 512) = make_uint4(0u, 0u, 0u, 0u);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a copy comes here again
       __syncwarp();
     }
