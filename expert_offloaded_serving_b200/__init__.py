@@ -36,7 +36,7 @@ EXPORTS = ("ft_blob_stride", "ft_blob_layout", "ft_last_error", "ft_create", "ft
            "ft_debug_device_wait", "ft_debug_host_wait_limit", "ft_debug_fail_copy", "ft_decode_geometry",
            "ft_debug_stack_epoch", "ft_flow_geometry", "ft_fp4_mma_probe", "ft_blob_layout_format",
            "ft_cache_prefetch", "ft_debug_stack_timeline", "ft_kv_workspace_bytes", "ft_kv_append", "ft_kv_attention",
-           "ft_kv_evict", "ft_kv_sync_status")
+           "ft_kv_evict", "ft_kv_sync_status", "ft_debug_kv_wait")
 FT_NOALLOC_SCRATCH_BYTES = 8 << 20
 FT_KV_BF16, FT_KV_E4M3 = 0, 1
 FT_KV_MASS = 1
@@ -136,6 +136,7 @@ def lib() -> C.CDLL:
         "ft_kv_attention": (ST, [C.POINTER(KvCache), P, I64, C.c_float, P, P, P, I64, U32, P]),
         "ft_kv_evict": (ST, [C.POINTER(KvCache), P, I32, P, I64, P]),
         "ft_kv_sync_status": (ST, [C.POINTER(KvCache), P]),
+        "ft_debug_kv_wait": (ST, [I32, I64, I64, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -520,3 +521,8 @@ def ft_kv_evict(kv: KvCache, budgets, recent, workspace, stream=None) -> None:
 
 def ft_kv_sync_status(kv: KvCache, stream=None) -> None:
     _check(lib().ft_kv_sync_status(C.byref(kv), _stream(stream)))
+
+
+def ft_debug_kv_wait(lanes, limit_us: int, arrive_us: int, stream=None) -> None:
+    """lanes int32 [blocks]."""
+    _check(lib().ft_debug_kv_wait(lanes.numel(), limit_us, arrive_us, _ptr(lanes, 4), _stream(stream)))

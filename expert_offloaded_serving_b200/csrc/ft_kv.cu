@@ -274,3 +274,16 @@ extern "C" ft_status ft_kv_sync_status(const ft_kv_cache* kv, void* stream) {
     return refuse(FT_ERR_INVALID, "the cache's contents: a page, length, position, axis or budget out of range");
   return FT_OK;
 }
+
+extern "C" ft_status ft_debug_kv_wait(int32_t blocks, int64_t limit_us, int64_t arrive_us, int32_t* lanes, void* stream) {
+  if (blocks < 1 || blocks > 1024) return refuse(FT_ERR_INVALID, "blocks %d not in [1, 1024]", blocks);
+  if (limit_us < 1 || limit_us > 1000000 || arrive_us > 1000000)
+    return refuse(FT_ERR_INVALID, "limit_us %lld not in [1, 1e6], or arrive_us %lld above 1e6", (long long)limit_us,
+                  (long long)arrive_us);
+  if (!lanes || !aligned(lanes, 4)) return refuse(FT_ERR_INVALID, "lanes is NULL or not on a 4-byte boundary");
+  Pointers at;
+  KV_TRY(at.begin());
+  KV_TRY(at.on("lanes", lanes));
+  return cu("ft_debug_kv_wait", ft::launch_kv_wait(blocks, (uint64_t)limit_us * 1000, arrive_us < 0 ? -1 : arrive_us * 1000,
+                                                   lanes, (cudaStream_t)stream));
+}

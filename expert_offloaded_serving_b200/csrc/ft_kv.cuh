@@ -91,6 +91,7 @@ int64_t kv_evict_workspace(const ft_kv_cache& c);
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool e4m3, bool adjacent, cudaStream_t s);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, bool e4m3, int device, int sms, cudaStream_t s);
+cudaError_t launch_kv_wait(int blocks, uint64_t limit_ns, int64_t arrive_ns, int32_t* lanes, cudaStream_t s);
 cudaError_t launch_kv_evict(const KvEvictArgs& a, int row_bytes, int device, int sms, cudaStream_t s);
 
 // Sets a kernel attribute once on each device (`done` has a bit for each; a second thread

@@ -134,9 +134,11 @@ struct SplitArgs {
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// Wait for phase `parity`; false after tc::kWaitNs.  The timer is read once the wait has
-// already taken many polls.
-__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity) {
+// Wait of a whole warp for phase `parity`; false after `limit` nanoseconds.  Votes decide, so that
+// its lanes always go the same way: after the wait they meet in products, shuffles and
+// votes that need every one of them.  A phase that one lane has seen stays complete until the warp
+// itself loads the stage again.  The timer is read once the wait has already taken many polls.
+__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, uint64_t limit = tc::kWaitNs) {
   const uint32_t at = smem_u32(bar);
   uint64_t since = 0;
   for (uint32_t n = 1;; n++) {
@@ -145,12 +147,33 @@ __device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity) {
                  : "=r"(ok)
                  : "r"(at), "r"(parity)
                  : "memory");
-    if (ok) return true;
+    if (__all_sync(0xffffffffu, ok)) return true;
     if ((n & 255) == 0) {
       const uint64_t now = tc::gtime();
       if (since == 0) since = now;
-      else if (now - since > tc::kWaitNs) return false;
+      if (__any_sync(0xffffffffu, now - since > limit)) return false;
     }
+  }
+}
+
+// The wait alone (ft_debug_kv_wait): warp 0 of a block waits on a barrier at which warp 1 arrives
+// after arrive_ns and a nanosecond for each block (never, if negative).
+__global__ void __launch_bounds__(64) k_kv_wait(uint64_t limit_ns, int64_t arrive_ns, int32_t* lanes) {
+  __shared__ __align__(8) uint64_t s_bar;
+  if (threadIdx.x == 0) tc::mbar_init(&s_bar, 1);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const bool there = wait_full(&s_bar, 0, limit_ns);
+    const int n = __syncthreads_count(there);
+    if (threadIdx.x == 0) lanes[blockIdx.x] = n;
+  } else {
+    if (threadIdx.x == 32 && arrive_ns >= 0) {
+      const uint64_t t0 = tc::gtime();
+      while (tc::gtime() - t0 < (uint64_t)arrive_ns + blockIdx.x) __nanosleep(20);
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&s_bar)) : "memory");
+    }
+    __syncwarp();
+    __syncthreads_count(false);
   }
 }
 
@@ -1115,6 +1138,11 @@ cudaError_t run_d(SplitArgs& a, int device, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_kv_wait(int blocks, uint64_t limit_ns, int64_t arrive_ns, int32_t* lanes, cudaStream_t s) {
+  k_kv_wait<<<blocks, 64, 0, s>>>(limit_ns, arrive_ns, lanes);
+  return cudaGetLastError();
+}
 
 int64_t kv_attn_workspace(const ft_kv_cache& c) {
   AttnWork w;

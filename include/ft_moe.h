@@ -668,6 +668,15 @@ FT_API ft_status ft_kv_evict(const ft_kv_cache* kv, const int32_t* budgets, int3
  * status word). */
 FT_API ft_status ft_kv_sync_status(const ft_kv_cache* kv, void* stream);
 
+/* Test hook for the bounded wait with which a warp of ft_kv_attention waits
+ * for its copies; it neither faults nor hangs a GPU.  `blocks` (1 .. 1024)
+ * blocks each wait at most limit_us (1 .. 1,000,000) microseconds for an
+ * arrival that comes after arrive_us (up to 1,000,000; negative: never)
+ * microseconds and a nanosecond for each block; lanes (dev int32 [blocks])
+ * gets the lanes of the waiting warp that saw it: all 32 or none.
+ * Errors: FT_ERR_INVALID, FT_ERR_CUDA. */
+FT_API ft_status ft_debug_kv_wait(int32_t blocks, int64_t limit_us, int64_t arrive_us, int32_t* lanes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
