@@ -686,7 +686,9 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
         for (int t = 0; t < NT; t++)
 #pragma unroll
           for (int e = 0; e < 2; e++) {
-            const bool gone = there != kFull && !((there >> (16 * t + 8 * e + g)) & 1u);
+            // With MASS neither may a column without a head have a score: against an infinite
+            // key its q of zero would give NaN, which goes to the workspace with the others.
+            const bool gone = (there != kFull && !((there >> (16 * t + 8 * e + g)) & 1u)) || (MASS && 8 * nb + j2 + i >= n_rows);
             s[t][nb][2 * e + i] = gone ? kNegInf : s[t][nb][2 * e + i] * qs[nb][i];
             x = fmaxf(x, s[t][nb][2 * e + i]);
           }
