@@ -272,9 +272,16 @@ constexpr int kMaxParts = 64;
 
 // A running maximum is replaced once a score passes it by this much (a factor of
 // 256): any reference would do for the sums, and most tiles then need neither
-// the maximum over the warp's lanes nor the rescaling of O.  p stays below 2^8,
-// within f16.
+// the maximum over the warp's lanes nor the rescaling of O.
+//
+// Over an E4M3 cache p meets v as f16, in two parts of 11 bits, and below 2^-14 f16 has fewer
+// bits, below 2^-25 none.  So the reference is taken kLift lower there: the largest p is
+// 2^7 to 2^15, still within f16 (a maximum that fp32 cannot lower by 7 only leaves p smaller), and what
+// is lost of a weight is 2^-22 of itself or 2^-32 of the largest, whichever is more.  The second part
+// costs 0 to 3 % (rows of 64 bytes with 16 heads a warp and heads of 256 with as many 11 %); one
+// part alone is 8.5e-4 from what fp32 gives, both 1e-4 and less.
 constexpr float kSlack = 8.0f;
+constexpr float kLift = 7.0f;
 
 // D: head_dim.  E4M3: the cache's format.  NB: blocks of 8 query heads of a
 // warp.  MASS: scores go to the workspace.
@@ -693,7 +700,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
             x = fmaxf(x, s[t][nb][2 * e + i]);
           }
         top[nb][i] = x;
-        over |= x - m[nb][i] > kSlack;  // the difference is exact where the two are near
+        over |= x - m[nb][i] > kSlack + (E4M3 ? kLift : 0.0f);  // the difference is exact where the two are near
       }
     if (MASS && at < args.w.tiles) {
       const int kept = NB == 2 ? 16 : score_rows(kv.G);  // of an entry
@@ -722,7 +729,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          x = fmaxf(x, m[nb][i]);
+          x = fmaxf(E4M3 ? x - kLift : x, m[nb][i]);
           const float down = x == m[nb][i] ? 1.0f : exp2_fast(m[nb][i] - x);
           m[nb][i] = x;
           l[nb][i] *= down;
@@ -745,9 +752,13 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
           const float x = exp2_fast(s[t][nb][2 * e] - z0), y = exp2_fast(s[t][nb][2 * e + 1] - z1);
           l[nb][0] += x;
           l[nb][1] += y;
+          // f16 keeps 11 bits of p, bf16 8: the rest goes through a second product
           if (E4M3) {
-            hi_p[t][nb][e] = transposed(f16x2(x, y));
-          } else {  // bf16 keeps 8 bits of p: the rest goes through a second product
+            const uint32_t u = f16x2(x, y);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u));
+            hi_p[t][nb][e] = transposed(u);
+            lo_p[t][nb][e] = transposed(f16x2(x - f.x, y - f.y));
+          } else {
             const uint32_t u = bf16x2(x, y);
             hi_p[t][nb][e] = transposed(u);
             lo_p[t][nb][e] = transposed(bf16x2(x - bf16_lo(u), y - bf16_hi(u)));
@@ -781,7 +792,10 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
             e4m3x4_to_f16(__byte_perm(x[2 * u], 0, 0x3120), a[0], a[1]);
             e4m3x4_to_f16(__byte_perm(x[2 * u + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
-            for (int nb = 0; nb < NB; nb++) mma<true>(o[2 * n + u][nb], a, hi_p[t][nb]);
+            for (int nb = 0; nb < NB; nb++) {
+              mma<true>(o[2 * n + u][nb], a, hi_p[t][nb]);
+              mma<true>(o[2 * n + u][nb], a, lo_p[t][nb]);
+            }
           }
         }
     }

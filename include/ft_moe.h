@@ -637,10 +637,13 @@ FT_API ft_status ft_kv_append(const ft_kv_cache* kv, int64_t T, const void* q, i
  *   that is not finite gives an infinity or NaN in its own element of out.
  *   With FT_KV_MASS, mass of entry i of KV head h += sum of p_i over the query
  *   heads that share h (mass must not be NULL).
- * Scores, softmax statistics and sums are fp32; out is rounded once to bf16.
- * For a BF16 cache p meets v in two bf16 parts (16 bits of p); for an E4M3
- * cache q is re-encoded as f16 with a power-of-two factor a head and p is
- * rounded to f16 (11 bits), both exact next to what E4M3 rounded.  The work
+ * Scores, softmax statistics and sums are fp32, added in the order of the
+ * entries within a part (n of them may cost up to n * 2^-23 of a sum); out is
+ * rounded once to bf16.
+ * For a BF16 cache p meets v in two bf16 parts (16 bits of p).  For an E4M3
+ * cache q is re-encoded as f16 with a power-of-two factor a head, exact for
+ * values down to 2^-28 of its largest one, and p meets v in two f16 parts: a
+ * weight is off by 2^-22 of itself or 2^-32 of the head's largest, whichever is more.  The work
  * is split over the entries of all sequences by their lengths on the device
  * and joined in a fixed order: the same inputs give the same bits on the same
  * kind of GPU.  Errors: FT_ERR_INVALID, FT_ERR_CUDA. */

@@ -35,3 +35,38 @@ def test_an_entry_whose_scores_are_all_minus_infinity_weighs_nothing(G, n):
             assert add[gone, 0] == 0 and got[gone, 0] == old[gone, 0]
         # a score is off by 68 x 2^-23 of at most 0.125 x 64 x 5 x 5 = 200 in size: weights by 2 x 200 x 68 x 2^-23 at most
         assert ((got - old - add).abs() <= add * 0.0035 + (old + add) * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("gap", [10.0, 17.3, 23.6, 25.1, 28.0])
+def test_one_entry_over_a_long_tail(gap, e4m3):
+    """The tail's weights are 2^-gap of the first entry's; 600 sequences share the pages, so that parts are long.
+
+    In the dims where the first entry's value is 0, out is the tail's share alone: each weight of it may be off by
+    2^-32 of the largest.  Sums: 600 rows of 4,096 tiles of 32 over 592 warps (BF16; E4M3 has twice as many) are 4,152 tiles a part at most,
+    2 steps and 2 parts of p each: 16,608 products added to O, each cutting off up to 2^-23 of it, 2^-8.98; a lane's
+    share of l is 4,152 x 4 additions that round by 2^-24, 2^-9.98.  Together 2^-8.4 < 2^-8; l alone 2^-9.98 < 2^-9."""
+    n, B, D, sums = 131072, 600, 128, 2.0 ** -8
+    c = Cache([n], 2, 1, D, 64, e4m3, seed=1, k_scale=1.0, v_scale=1.0625)
+    v = 1.875 if e4m3 else 1.9921875  # 1.9921875 each way, a value of bf16
+    at = c.place(0, torch.arange(n, device="cuda"))
+    x = torch.zeros(n, 1, D, device="cuda")
+    x[0, 0, 0] = 1.0
+    c.k[at] = c.stored(x, 1.0)
+    x = torch.full((n, 1, D), v, device="cuda")
+    x[0, 0, :32] = 0.0
+    c.v[at] = c.stored(x, 1.0)
+    c.table = c.table.expand(B, -1).contiguous()
+    c.lengths = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    q = torch.zeros(B, 2, D, dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = 1.0  # head 1 sees all entries alike
+    out, lse = call(c, q, gap * math.log(2))
+    tail = (n - 1) * 2.0 ** -gap
+    want = 1.9921875 * tail / (1 + tail)
+    off = (out[:, 0, :32].double() - want).abs().max().item()
+    assert off <= want * (2.0 ** -8 + sums) + n * 2.0 ** -32 * 1.9921875, off / want
+    assert (out[:, 0, 32:].double() - 1.9921875).abs().max() <= 1.9921875 * (2.0 ** -8 + sums)
+    assert (lse[:, 0].double() - gap * math.log(2) - math.log1p(tail)).abs().max() <= 2.0 ** -9
+    want = 1.9921875 * (n - 1) / n
+    assert (out[:, 1, :32].double() - want).abs().max() <= want * (2.0 ** -8 + sums)
+    assert (lse[:, 1].double() - math.log(n)).abs().max() <= 2.0 ** -9
