@@ -36,7 +36,7 @@ EXPORTS = ("ft_blob_stride", "ft_blob_layout", "ft_last_error", "ft_create", "ft
            "ft_debug_device_wait", "ft_debug_host_wait_limit", "ft_debug_fail_copy", "ft_decode_geometry",
            "ft_debug_stack_epoch", "ft_flow_geometry", "ft_fp4_mma_probe", "ft_blob_layout_format",
            "ft_cache_prefetch", "ft_debug_stack_timeline", "ft_kv_workspace_bytes", "ft_kv_append", "ft_kv_attention",
-           "ft_kv_evict", "ft_kv_sync_status", "ft_debug_kv_wait")
+           "ft_kv_evict", "ft_kv_sync_status", "ft_debug_kv_wait", "ft_kv_geometry")
 FT_NOALLOC_SCRATCH_BYTES = 8 << 20
 FT_KV_BF16, FT_KV_E4M3 = 0, 1
 FT_KV_MASS = 1
@@ -132,6 +132,7 @@ def lib() -> C.CDLL:
         "ft_fp4_mma_probe": (ST, [I64, P, P, C.POINTER(I32), P]),
         "ft_decode_geometry": (ST, [I32, I32, I32, C.POINTER(I64)]),
         "ft_kv_workspace_bytes": (ST, [C.POINTER(KvCache), C.POINTER(I64)]),
+        "ft_kv_geometry": (ST, [C.POINTER(KvCache), I64, I32, C.POINTER(I64)]),
         "ft_kv_append": (ST, [C.POINTER(KvCache), I64, P, I64, P, I64, P, I64, P, P, I32, P, P, I32, P, U32, P]),
         "ft_kv_attention": (ST, [C.POINTER(KvCache), P, I64, C.c_float, P, P, P, I64, U32, P]),
         "ft_kv_evict": (ST, [C.POINTER(KvCache), P, I32, P, I64, P]),
@@ -465,6 +466,13 @@ def ft_kv_workspace_bytes(kv: KvCache) -> int:
     n = I64()
     _check(lib().ft_kv_workspace_bytes(C.byref(kv), C.byref(n)))
     return n.value
+
+
+def ft_kv_geometry(kv: KvCache, tiles: int, sms: int = 148) -> tuple[int, int, int, int]:
+    """(entries of a tile, tiles of a chunk, chunks used, chunks there are)"""
+    out = (I64 * 4)()
+    _check(lib().ft_kv_geometry(C.byref(kv), tiles, sms, out))
+    return tuple(out)
 
 
 def ft_kv_append(kv: KvCache, q, k, v, cu_new, positions, inv_freq, axis, q_out, flags=0, stream=None) -> None:

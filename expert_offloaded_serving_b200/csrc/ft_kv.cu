@@ -169,6 +169,16 @@ extern "C" ft_status ft_kv_workspace_bytes(const ft_kv_cache* kv, int64_t* bytes
   return FT_OK;
 }
 
+extern "C" ft_status ft_kv_geometry(const ft_kv_cache* kv, int64_t tiles, int32_t sms, int64_t out[4]) {
+  KV_TRY(check_shape(kv));
+  if (!out) return refuse(FT_ERR_INVALID, "out is NULL");
+  if (kv->n_seqs < 1) return refuse(FT_ERR_INVALID, "n_seqs 0 has no split");
+  if (tiles < 0 || tiles >= (int64_t)1 << 30) return refuse(FT_ERR_INVALID, "tiles %lld not in [0, 2^30)", (long long)tiles);
+  if (sms < 16 || sms > 1024) return refuse(FT_ERR_INVALID, "sms %d not in [16, 1024]", sms);
+  ft::kv_geometry(*kv, (int)tiles, sms, out);
+  return FT_OK;
+}
+
 extern "C" ft_status ft_kv_append(const ft_kv_cache* kv, int64_t T, const void* q, int64_t q_stride, const void* k,
                                   int64_t k_stride, const void* v, int64_t v_stride, const int32_t* cu_new,
                                   const int32_t* positions, int32_t n_axes, const double* inv_freq,

@@ -127,7 +127,6 @@ struct SplitArgs {
   KvAttnArgs a;
   AttnWork w;
   int groups;      // of 16 query heads, a KV head
-  float per_chunk;  // 1 / chunks of the launch
   float per_part;  // 1 / (rows x kMaxParts)
   int box_shift;  // box_rows = 1 << box_shift: a tile's rows, or a page's where pages are smaller
 };
@@ -269,6 +268,16 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // join of one more part does not), but one row's hundreds of parts are not (4,000
 // entries, two KV heads of 256: 250 parts 17.3 us, 84 parts 12.7).
 constexpr int kMaxParts = 64;
+inline float part_share(int n_seqs, int n_kv) { return 1.0f / ((float)n_seqs * (float)n_kv * kMaxParts); }
+
+// Tiles of a chunk: an equal share (all of them lie on the chunks there are), more for short rows.
+__host__ __device__ inline int chunk_tiles(int total, int chunks, float per_part) {
+  const int equal = (int)(((uint32_t)total + (uint32_t)chunks - 1u) / (uint32_t)chunks);
+  const int fewer = (int)((float)total * per_part);
+  const int least = fewer < 4 ? fewer : 4;
+  const int n = equal > least ? equal : least;
+  return n > 1 ? n : 1;
+}
 
 // A running maximum is replaced once a score passes it by this much (a factor of
 // 256): any reference would do for the sums, and most tiles then need neither
@@ -316,19 +325,12 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
   const int groups = NB == 1 ? 1 : args.groups;
   const int warps = (int)gridDim.x * R::kWarps, chunks = warps / groups;
   const int c = j / groups, gi = j - c * groups;  // the warp's chunk and group; c can be `chunks`: nothing there
-  auto chunk_of = [&](int total) {  // ceil(total / chunks), exact: the estimate is at most one off
-    int n = (int)((float)total * args.per_chunk);
-    n += n * chunks < total;
-    n += n * chunks < total;
-    n -= (n - 1) * chunks >= total && n > 0;
-    return max(max(n, 1), min(4, (int)((float)total * args.per_part)));
-  };
   // The tiles of the batch are counted, cut, and the chunk's first one is looked up: its
   // sequence, and that one's first tile in the batch.
   Place cons;
   int base, total, chunk, lo, hi;
   auto cut = [&] {
-    chunk = chunk_of(total);
+    chunk = chunk_tiles(total, chunks, args.per_part);
     lo = (int)min((int64_t)c * chunk, (int64_t)total);
     hi = min(lo + chunk, total);
   };
@@ -1121,8 +1123,7 @@ cudaError_t run(SplitArgs& a, int device, int sms, cudaStream_t s) {
   const uint64_t rows = (uint64_t)kv.n_pages * kv.Hkv << kv.page_shift;
   a.box_shift = R::kTile == 32 ? 5 : 4;
   if (kv.page_shift < a.box_shift) a.box_shift = kv.page_shift;
-  a.per_chunk = 1.0f / (float)(sms * R::kWarps / a.groups);
-  a.per_part = 1.0f / ((float)kv.n_seqs * (float)kv.Hkv * kMaxParts);
+  a.per_part = part_share(kv.n_seqs, kv.Hkv);
   const uint32_t deep = (1 << a.box_shift) == R::kTile ? R::kBoxes : 1;
   if (encode_tmap_rows(&a.k_map, kv.k, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift, deep) != FT_OK ||
       encode_tmap_rows(&a.v_map, kv.v, D * (E4M3 ? 1 : 2), rows, R::kBox, 1u << a.box_shift, deep) != FT_OK)
@@ -1158,6 +1159,15 @@ cudaError_t run_d(SplitArgs& a, int device, int sms, cudaStream_t s) {
 cudaError_t launch_kv_wait(int blocks, uint64_t limit_ns, int64_t arrive_ns, int32_t* lanes, cudaStream_t s) {
   k_kv_wait<<<blocks, 64, 0, s>>>(limit_ns, arrive_ns, lanes);
   return cudaGetLastError();
+}
+
+void kv_geometry(const ft_kv_cache& c, int total, int sms, int64_t out[4]) {
+  const int row_bytes = c.head_dim * (c.format == FT_KV_E4M3 ? 1 : 2);
+  const int chunks = (sms < kKvMaxSms ? sms : kKvMaxSms) * warps_of(row_bytes) / groups_of(c.n_heads / c.n_kv_heads);
+  out[0] = tile_of(row_bytes);
+  out[1] = chunk_tiles(total, chunks, part_share(c.n_seqs, c.n_kv_heads));
+  out[2] = (total + out[1] - 1) / out[1];
+  out[3] = chunks;
 }
 
 int64_t kv_attn_workspace(const ft_kv_cache& c) {

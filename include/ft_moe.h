@@ -594,6 +594,13 @@ typedef struct {
  * ft_kv_evict).  FT_ERR_INVALID on a bad shape. */
 FT_API ft_status ft_kv_workspace_bytes(const ft_kv_cache* kv, int64_t* bytes);
 
+/* How ft_kv_attention splits a batch of `tiles` tiles (below 2^30; a tile is
+ * up to out[0] entries of one sequence and KV head) on a GPU of `sms` SMs (16 to
+ * 1024; host only, no device needed): out[0] = entries of a tile, out[1] =
+ * tiles of a chunk, out[2] = chunks used, out[3] = chunks there are; a chunk is a warp's, or
+ * one warp's for every 16 query heads a KV head.  FT_ERR_INVALID on a bad shape. */
+FT_API ft_status ft_kv_geometry(const ft_kv_cache* kv, int64_t tiles, int32_t sms, int64_t out[4]);
+
 /* Rotate the new tokens' queries and keys by their positions and write keys
  * and values into the cache, before the step's attention.
  *   T        new tokens.  The caller has already advanced lengths to count

@@ -1,8 +1,10 @@
 """More argument checks of the key-value cache calls at the edges of what they take, without a GPU."""
+import ctypes as C
+
 import pytest
 
 import expert_offloaded_serving_b200 as ft
-from test_kv_host import OUT, refused
+from test_kv_host import OUT, cache, refused
 
 
 @pytest.mark.parametrize("args,what", [((0, 10, 10, OUT), "blocks"), ((1025, 10, 10, OUT), "blocks"), ((4, 0, 10, OUT), "limit_us"),
@@ -10,3 +12,28 @@ from test_kv_host import OUT, refused
                                        ((4, 10, 10, None), "lanes"), ((4, 10, 10, OUT + 2), "lanes")])
 def test_the_wait_hook_refuses(args, what):
     refused(ft.lib().ft_debug_kv_wait(*args, None), what)
+
+
+@pytest.mark.parametrize("shape", [
+    dict(head_dim=256, n_heads=1024, n_kv_heads=1), dict(head_dim=64, n_heads=1024, n_kv_heads=1),
+    dict(head_dim=64, n_heads=1000, n_kv_heads=2, format=ft.FT_KV_E4M3), dict(head_dim=128, n_heads=32, n_kv_heads=8),
+    dict(head_dim=96, n_heads=33, n_kv_heads=3, format=ft.FT_KV_E4M3)])
+@pytest.mark.parametrize("sms", [16, 108, 148, 160, 200])
+def test_the_split_covers_every_tile(shape, sms):
+    """All tiles lie on the chunks there are, up to the 2^30 the shapes allow; none is larger than an equal share
+    needs, but for the 4 tiles that a short row's chunks may have."""
+    kv = cache(n_seqs=1, **shape)
+    for tiles in [*range(0, 700, 13), 4735, 4736, 4737, 99999, (1 << 24) + 1, 268485103, 268485104, 536970461, (1 << 30) - 1,
+                  *range(1 << 28, 1 << 30, 9999991)]:
+        tile, chunk, used, there = ft.ft_kv_geometry(kv, tiles, sms)
+        assert tile in (16, 32) and chunk >= 1 and used <= there
+        assert used * chunk >= tiles > (used - 1) * chunk or tiles == used == 0
+        assert chunk <= max(4, -(-tiles // there))
+
+
+@pytest.mark.parametrize("tiles,sms,what", [(-1, 148, "tiles"), (1 << 30, 148, "tiles"), (5, 15, "sms"), (5, 1025, "sms")])
+def test_the_split_refuses(tiles, sms, what):
+    refused(ft.lib().ft_kv_geometry(C.byref(cache()), tiles, sms, (ft.I64 * 4)()), what)
+    refused(ft.lib().ft_kv_geometry(C.byref(cache()), 5, 148, None), "NULL")
+    refused(ft.lib().ft_kv_geometry(C.byref(cache(n_seqs=0)), 5, 148, (ft.I64 * 4)()), "n_seqs")
+    refused(ft.lib().ft_kv_geometry(C.byref(cache(head_dim=7)), 5, 148, (ft.I64 * 4)()), "head_dim")
