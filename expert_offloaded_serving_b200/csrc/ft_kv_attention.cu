@@ -486,8 +486,9 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
     const float unit = args.a.scale * 1.4426950408889634f * kv.k_scale;
 #pragma unroll
     for (int nb = 0; nb < NB; nb++) {
-      const bool real = g + 8 * nb < n_rows;
-      const uint16_t* src = args.a.q + (int64_t)b * args.a.q_stride + (int64_t)(head0 + (real ? g + 8 * nb : 0)) * D;
+      // Columns without a head repeat the first one: add_mass takes their weights out by an lse of +inf,
+      // and the scores of a q of zero would be NaN against an infinite key whatever the heads' own are.
+      const uint16_t* src = args.a.q + (int64_t)b * args.a.q_stride + (int64_t)(head0 + (g + 8 * nb < n_rows ? g + 8 * nb : 0)) * D;
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         m[nb][i] = kNegInf;
@@ -499,10 +500,9 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
         // E4M3: the 16 contraction steps of an mma take the dims 4i, 4i+1 (first
         // half) and 4i+2, 4i+3 (second half) of each lane i of a quad: the order in
         // which ldmatrix hands out the bytes of a key.
-        const uint2 x = !real ? make_uint2(0u, 0u)
-                        : E4M3 ? *reinterpret_cast<const uint2*>(src + ks * 16 + 2 * j2)
-                               : make_uint2(*reinterpret_cast<const uint32_t*>(src + ks * 16 + j2),
-                                            *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + j2));
+        const uint2 x = E4M3 ? *reinterpret_cast<const uint2*>(src + ks * 16 + 2 * j2)
+                             : make_uint2(*reinterpret_cast<const uint32_t*>(src + ks * 16 + j2),
+                                          *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + j2));
         q[ks][nb][0] = x.x;
         q[ks][nb][1] = x.y;
       }
@@ -695,9 +695,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
         for (int t = 0; t < NT; t++)
 #pragma unroll
           for (int e = 0; e < 2; e++) {
-            // With MASS neither may a column without a head have a score: against an infinite
-            // key its q of zero would give NaN, which goes to the workspace with the others.
-            const bool gone = (there != kFull && !((there >> (16 * t + 8 * e + g)) & 1u)) || (MASS && 8 * nb + j2 + i >= n_rows);
+            const bool gone = there != kFull && !((there >> (16 * t + 8 * e + g)) & 1u);
             s[t][nb][2 * e + i] = gone ? kNegInf : s[t][nb][2 * e + i] * qs[nb][i];
             x = fmaxf(x, s[t][nb][2 * e + i]);
           }
