@@ -190,7 +190,7 @@ extern "C" ft_status ft_kv_append(const ft_kv_cache* kv, int64_t T, const void* 
   if (flags & ~FT_ROPE_ADJACENT) return refuse(FT_ERR_INVALID, "unknown flags 0x%x", flags);
   if (rot_dim < 0 || rot_dim > kv->head_dim || rot_dim % 16)
     return refuse(FT_ERR_INVALID, "rot_dim %d is not a multiple of 16 from 0 to head_dim", rot_dim);
-  if (n_axes < 0 || n_axes > 4 || ((rot_dim || kv->pos) && n_axes < 1))
+  if (n_axes < 0 || n_axes > 4 || ((rot_dim || kv->pos || positions) && n_axes < 1))
     return refuse(FT_ERR_INVALID, "n_axes %d not in [1, 4]", n_axes);
   if (T == 0 || kv->n_seqs == 0) return FT_OK;
   if (!k || !v || (q == nullptr) != (q_out == nullptr)) return refuse(FT_ERR_INVALID, "NULL k or v, or one of q and q_out");

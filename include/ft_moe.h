@@ -615,7 +615,8 @@ FT_API ft_status ft_kv_geometry(const ft_kv_cache* kv, int64_t tiles, int32_t sm
  *            multiples of 8 (q, k and v may be parts of one projection's
  *            output).  q and q_out may both be NULL: keys and values only.
  *   positions dev int32 [n_axes][T], not negative: one axis for text, three
- *            (time, height, width) for images and video; n_axes 1 to 4.
+ *            (time, height, width) for images and video; n_axes 1 to 4.  NULL (n_axes 0)
+ *            where nothing turns and the cache has no pos.
  *   inv_freq dev fp64 [rot_dim/2], axis dev int32 [rot_dim/2]: pair i turns
  *            by positions[axis[i]][t] * inv_freq[i] radians, so that any
  *            base, scaling and order of the axes' sections can be laid out

@@ -4,7 +4,7 @@ import ctypes as C
 import pytest
 
 import expert_offloaded_serving_b200 as ft
-from test_kv_host import OUT, cache, refused
+from test_kv_host import OUT, append, cache, refused
 
 
 @pytest.mark.parametrize("args,what", [((0, 10, 10, OUT), "blocks"), ((1025, 10, 10, OUT), "blocks"), ((4, 0, 10, OUT), "limit_us"),
@@ -37,3 +37,9 @@ def test_the_split_refuses(tiles, sms, what):
     refused(ft.lib().ft_kv_geometry(C.byref(cache()), 5, 148, None), "NULL")
     refused(ft.lib().ft_kv_geometry(C.byref(cache(n_seqs=0)), 5, 148, (ft.I64 * 4)()), "n_seqs")
     refused(ft.lib().ft_kv_geometry(C.byref(cache(head_dim=7)), 5, 148, (ft.I64 * 4)()), "head_dim")
+
+
+def test_positions_without_an_axis_are_refused():
+    """Nothing turns and nothing is stored, so no axis is needed; but positions of none of them hold no token's."""
+    refused(append(cache(pos=None), rot=0, inv=None, axis=None, axes=0), "n_axes")
+    assert append(cache(pos=None), T=0, cu=OUT, rot=0, inv=None, axis=None, axes=0, pos=None) == ft.FT_OK
