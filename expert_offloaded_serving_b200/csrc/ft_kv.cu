@@ -58,6 +58,8 @@ ft_status check_shape(const ft_kv_cache* c) {
     return refuse(FT_ERR_INVALID, "format %d is not FT_KV_BF16 or FT_KV_E4M3", c->format);
   if (!(c->k_scale > 0) || !(c->v_scale > 0) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
     return refuse(FT_ERR_INVALID, "k_scale and v_scale must be positive and finite");
+  if (!std::isfinite(1.0f / c->k_scale) || !std::isfinite(1.0f / c->v_scale))
+    return refuse(FT_ERR_INVALID, "k_scale or v_scale is 2^-128 or less: its reciprocal is not finite");
   if (c->format == FT_KV_BF16 && (c->k_scale != 1.0f || c->v_scale != 1.0f))
     return refuse(FT_ERR_INVALID, "k_scale and v_scale of a BF16 cache are 1");
   return FT_OK;

@@ -569,7 +569,7 @@ typedef struct {
                             times its 16ths below 2^30 */
   int64_t n_pages;       /* pages of the pools; n_pages * n_kv_heads * page_size < 2^31 */
   int32_t format;        /* FT_KV_BF16 or FT_KV_E4M3 */
-  float k_scale;         /* what one unit of a stored key / value stands for (E4M3: positive and finite; */
+  float k_scale;         /* what one unit of a stored key / value stands for (E4M3: positive, finite as its reciprocal; */
   float v_scale;         /*   BF16: 1) */
   void* k;               /* dev [n_pages][n_kv_heads][page_size][D] */
   void* v;               /* dev, the same */

@@ -4,7 +4,7 @@ import ctypes as C
 import pytest
 
 import expert_offloaded_serving_b200 as ft
-from test_kv_host import OUT, append, cache, refused
+from test_kv_host import OUT, append, attend, cache, evict, refused
 
 
 @pytest.mark.parametrize("args,what", [((0, 10, 10, OUT), "blocks"), ((1025, 10, 10, OUT), "blocks"), ((4, 0, 10, OUT), "limit_us"),
@@ -43,3 +43,13 @@ def test_positions_without_an_axis_are_refused():
     """Nothing turns and nothing is stored, so no axis is needed; but positions of none of them hold no token's."""
     refused(append(cache(pos=None), rot=0, inv=None, axis=None, axes=0), "n_axes")
     assert append(cache(pos=None), T=0, cu=OUT, rot=0, inv=None, axis=None, axes=0, pos=None) == ft.FT_OK
+
+
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+def test_a_scale_without_a_finite_reciprocal_is_refused(which):
+    """What is stored is the value times 1 / scale: infinity would make NaN of a zero."""
+    for scale in (2.0 ** -149, 2.0 ** -129, 2.0 ** -128):  # 2^128 is past fp32
+        for call in (append, attend, evict):
+            refused(call(cache(format=ft.FT_KV_E4M3, **{which: scale})), "reciprocal")
+    for scale in (2.0 ** -127, 2.0 ** 127):
+        assert append(cache(format=ft.FT_KV_E4M3, **{which: scale}), T=0, cu=OUT) == ft.FT_OK
