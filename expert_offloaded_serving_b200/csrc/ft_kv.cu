@@ -232,6 +232,8 @@ extern "C" ft_status ft_kv_attention(const ft_kv_cache* kv, const void* q, int64
   if (flags & ~FT_KV_MASS) return refuse(FT_ERR_INVALID, "unknown flags 0x%x", flags);
   if ((flags & FT_KV_MASS) && !kv->mass) return refuse(FT_ERR_INVALID, "FT_KV_MASS without a mass pool");
   if (!std::isfinite(scale)) return refuse(FT_ERR_INVALID, "scale is not finite");
+  if (!std::isfinite(scale * 1.4426950408889634f * kv->k_scale))
+    return refuse(FT_ERR_INVALID, "scale %g times log2(e) and k_scale %g is not finite", scale, kv->k_scale);
   if (kv->n_seqs == 0) return FT_OK;
   if (!q || !out) return refuse(FT_ERR_INVALID, "NULL q or out");
   const int64_t width = (int64_t)kv->n_heads * kv->head_dim;

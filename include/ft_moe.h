@@ -637,6 +637,7 @@ FT_API ft_status ft_kv_append(const ft_kv_cache* kv, int64_t T, const void* q, i
 /* Attention of one new token a sequence over its cached entries:
  *   p = softmax over the entries i of (scale * q . k_i), out = sum_i p_i v_i,
  *   lse = log sum_i exp(scale * q . k_i).
+ *   scale * log2(e) * k_scale is finite in fp32.
  *   q dev bf16, row b at q + b*q_stride elements (a multiple of 8), [n_heads][D]
  *   dense within; out dev bf16 [n_seqs][n_heads][D], must not overlap q;
  *   lse dev fp32 [n_seqs][n_heads] or NULL.  A row without entries gives

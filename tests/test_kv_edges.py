@@ -53,3 +53,10 @@ def test_a_scale_without_a_finite_reciprocal_is_refused(which):
             refused(call(cache(format=ft.FT_KV_E4M3, **{which: scale})), "reciprocal")
     for scale in (2.0 ** -127, 2.0 ** 127):
         assert append(cache(format=ft.FT_KV_E4M3, **{which: scale}), T=0, cu=OUT) == ft.FT_OK
+
+
+def test_a_scale_that_leaves_fp32_is_refused():
+    """Scores are taken in units of log2(e) and of k_scale: scale times both has to be finite, or a score of 0 is NaN."""
+    refused(attend(scale=3e38), "scale")
+    refused(attend(cache(format=ft.FT_KV_E4M3, k_scale=2.0 ** 100), scale=-2.0 ** 28), "scale")
+    refused(attend(scale=2e38, work=None), "workspace")  # 2.9e38 fits, the next check speaks
