@@ -439,22 +439,31 @@ def make_kv(n_heads, k, v, block_table, lengths, mass=None, pos=None, k_scale=1.
                  _ptr(mass, 4), _ptr(pos, 4), _ptr(block_table, 4), _ptr(lengths, 4), _ptr(status, 4))
     kv.tensors = (k, v, mass, pos, block_table, lengths, status)
     kv.dims = (d, n_heads, n_kv, block_table.shape[0])
+    import torch
+    kv.types = (torch.bfloat16, torch.int32, torch.float32, torch.float64)
     kv.ref = C.byref(kv)
     return kv
 
 
-def _dev(t, size: int) -> int | None:
-    """_ptr of a tensor (or None), by the short way where it is as it should be: these calls take microseconds."""
+def _dev(t, name, dtype) -> int | None:
+    """Address of a dense tensor of that type (or None): these calls take microseconds, so it is the short way."""
     if t is None:
         return None
-    if t.element_size() == size and t.is_contiguous():
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} of dtype {t.dtype}: {dtype}")
+    if t.is_contiguous():
         return t.data_ptr()
-    return _ptr(t, size)
+    return _ptr(t)
 
 
-def _rows(t, name, rows, heads, d) -> tuple[int, int]:
+def _work(t) -> int:
+    """Address of a workspace, bytes of any type."""
+    return t.data_ptr() if t.element_size() == 1 and t.is_contiguous() else _ptr(t, 1)
+
+
+def _rows(t, name, rows, heads, d, bf16) -> tuple[int, int]:
     """Address and row stride (elements) of q, k or v [rows][heads][d]; rows may be apart, a row is dense."""
-    if t.shape != (rows, heads, d) or t.element_size() != 2:
+    if t.shape != (rows, heads, d) or t.dtype is not bf16:
         raise ValueError(f"{name} {tuple(t.shape)} {t.dtype}: bf16 [{rows}][{heads}][{d}]")
     row, head, one = t.stride()
     if one != 1 or (head != d and heads > 1):
@@ -480,10 +489,11 @@ def ft_kv_append(kv: KvCache, q, k, v, cu_new, positions, inv_freq, axis, q_out,
     [n_seqs+1] or None, positions int32 [axes][T], inv_freq float64 and axis int32 [rot_dim/2] (or None, both: no
     rotation)."""
     d, hq, hk, n_seqs = kv.dims
+    bf16, i32, _, f64 = kv.types
     T = k.shape[0]
-    kp, ks = _rows(k, "k", T, hk, d)
-    vp, vs = _rows(v, "v", T, hk, d)
-    qp, qs = _rows(q, "q", T, hq, d) if q is not None else (None, 0)
+    kp, ks = _rows(k, "k", T, hk, d, bf16)
+    vp, vs = _rows(v, "v", T, hk, d, bf16)
+    qp, qs = _rows(q, "q", T, hq, d, bf16) if q is not None else (None, 0)
     if q_out is not None and q_out.shape != (T, hq, d):
         raise ValueError(f"q_out of shape {tuple(q_out.shape)}: {(T, hq, d)}")
     if cu_new is not None and cu_new.shape != (n_seqs + 1,):
@@ -496,8 +506,9 @@ def ft_kv_append(kv: KvCache, q, k, v, cu_new, positions, inv_freq, axis, q_out,
     half = 0 if inv_freq is None else inv_freq.shape[0]
     if (inv_freq is None) != (axis is None) or (axis is not None and axis.shape != (half,)):
         raise ValueError("inv_freq and axis: [rot_dim/2] each, or None")
-    st = lib().ft_kv_append(kv.ref, T, qp, qs, kp, ks, vp, vs, _dev(cu_new, 4), _dev(positions, 4), axes,
-                            _dev(inv_freq, 8), _dev(axis, 4), 2 * half, _dev(q_out, 2), flags, _stream(stream))
+    st = lib().ft_kv_append(kv.ref, T, qp, qs, kp, ks, vp, vs, _dev(cu_new, "cu_new", i32),
+                            _dev(positions, "positions", i32), axes, _dev(inv_freq, "inv_freq", f64),
+                            _dev(axis, "axis", i32), 2 * half, _dev(q_out, "q_out", bf16), flags, _stream(stream))
     if st:
         _check(st)
 
@@ -506,13 +517,14 @@ def ft_kv_attention(kv: KvCache, q, scale, out, lse, workspace, flags=0, stream=
     """q [n_seqs][n_heads][D] (rows may be apart), out dense of that shape, lse float32 [n_seqs][n_heads] or None,
     workspace uint8."""
     d, hq, _, n_seqs = kv.dims
-    qp, qs = _rows(q, "q", n_seqs, hq, d)
+    bf16, _, f32, _ = kv.types
+    qp, qs = _rows(q, "q", n_seqs, hq, d, bf16)
     if out.shape != (n_seqs, hq, d):
         raise ValueError(f"out of shape {tuple(out.shape)}: {(n_seqs, hq, d)}")
     if lse is not None and lse.shape != (n_seqs, hq):
         raise ValueError(f"lse of shape {tuple(lse.shape)}: {(n_seqs, hq)}")
-    st = lib().ft_kv_attention(kv.ref, qp, qs, scale, _dev(out, 2), _dev(lse, 4), _dev(workspace, 1), workspace.numel(),
-                               flags, _stream(stream))
+    st = lib().ft_kv_attention(kv.ref, qp, qs, scale, _dev(out, "out", bf16), _dev(lse, "lse", f32),
+                               _work(workspace), workspace.numel(), flags, _stream(stream))
     if st:
         _check(st)
 
@@ -522,7 +534,8 @@ def ft_kv_evict(kv: KvCache, budgets, recent, workspace, stream=None) -> None:
     n_seqs = kv.dims[3]
     if budgets.shape != (n_seqs,):
         raise ValueError(f"budgets of shape {tuple(budgets.shape)}: {(n_seqs,)}")
-    st = lib().ft_kv_evict(kv.ref, _dev(budgets, 4), recent, _dev(workspace, 1), workspace.numel(), _stream(stream))
+    st = lib().ft_kv_evict(kv.ref, _dev(budgets, "budgets", kv.types[1]), recent, _work(workspace), workspace.numel(),
+                           _stream(stream))
     if st:
         _check(st)
 
@@ -533,4 +546,6 @@ def ft_kv_sync_status(kv: KvCache, stream=None) -> None:
 
 def ft_debug_kv_wait(lanes, limit_us: int, arrive_us: int, stream=None) -> None:
     """lanes int32 [blocks]."""
+    if str(lanes.dtype).rpartition(".")[2] != "int32":
+        raise ValueError(f"lanes of dtype {lanes.dtype}: int32")
     _check(lib().ft_debug_kv_wait(lanes.numel(), limit_us, arrive_us, _ptr(lanes, 4), _stream(stream)))

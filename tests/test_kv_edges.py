@@ -2,9 +2,10 @@
 import ctypes as C
 
 import pytest
+import torch
 
 import expert_offloaded_serving_b200 as ft
-from test_kv_host import OUT, append, attend, cache, evict, refused
+from test_kv_host import OUT, append, attend, cache, evict, refused, tensors
 
 
 @pytest.mark.parametrize("args,what", [((0, 10, 10, OUT), "blocks"), ((1025, 10, 10, OUT), "blocks"), ((4, 0, 10, OUT), "limit_us"),
@@ -60,3 +61,31 @@ def test_a_scale_that_leaves_fp32_is_refused():
     refused(attend(scale=3e38), "scale")
     refused(attend(cache(format=ft.FT_KV_E4M3, k_scale=2.0 ** 100), scale=-2.0 ** 28), "scale")
     refused(attend(scale=2e38, work=None), "workspace")  # 2.9e38 fits, the next check speaks
+
+
+def test_binding_refuses_other_types_of_the_same_size():
+    """fp16 bits read as bf16, or float32 ones as int32, would give wrong numbers without a word."""
+    kv = ft.make_kv(8, **tensors())
+    bf, half, i32, f32 = torch.bfloat16, torch.float16, torch.int32, torch.float32
+    work = torch.zeros(8, dtype=torch.uint8)
+
+    def rows(heads, dtype):
+        return torch.zeros(3, heads, 64, dtype=dtype)
+
+    def append(q=bf, k=bf, v=bf, cu=i32, pos=i32, inv=torch.float64, axis=i32, q_out=bf):
+        ft.ft_kv_append(kv, rows(8, q), rows(2, k), rows(2, v), torch.zeros(4, dtype=cu), torch.zeros(1, 3, dtype=pos),
+                        torch.zeros(32, dtype=inv), torch.zeros(32, dtype=axis), rows(8, q_out), 0, 0)
+
+    for kw in (dict(q=half), dict(k=half), dict(v=torch.int16), dict(q_out=half), dict(cu=f32), dict(pos=f32),
+               dict(inv=torch.int64), dict(axis=f32)):
+        with pytest.raises(ValueError, match=str(*kw.values())):
+            append(**kw)
+    for q, out, lse in ((half, bf, f32), (bf, half, f32), (bf, bf, i32)):
+        with pytest.raises(ValueError, match="float16" if half in (q, out) else "int32"):
+            ft.ft_kv_attention(kv, rows(8, q), 0.1, rows(8, out), torch.zeros(3, 8, dtype=lse), work, 0, 0)
+    with pytest.raises(ValueError, match="float32"):
+        ft.ft_kv_evict(kv, torch.zeros(3), 0, work, 0)
+    with pytest.raises(ValueError, match="float32"):
+        ft.ft_debug_kv_wait(torch.zeros(3), 10, 10, 0)
+    with pytest.raises(ft.FtError, match="workspace"):  # the right types pass to the library's own checks
+        ft.ft_kv_attention(kv, rows(8, bf), 0.1, rows(8, bf), torch.zeros(3, 8), work, 0, 0)
