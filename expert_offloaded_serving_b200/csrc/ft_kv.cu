@@ -220,10 +220,12 @@ extern "C" ft_status ft_kv_append(const ft_kv_cache* kv, int64_t T, const void* 
   KV_TRY(at.on("inv_freq", inv_freq));
   KV_TRY(at.on("axis", axis));
   KV_TRY(at.on("q_out", q_out));
+  int sms = 0;
+  KV_TRY(sm_count(at.device, sms));
   const ft::KvAppendArgs a{vw,       T,         (const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v,
                            q_stride, k_stride,  v_stride,           cu_new,             positions,
                            n_axes,   inv_freq,  axis,               rot_dim,            (uint16_t*)q_out};
-  return cu("ft_kv_append", ft::launch_kv_append(a, kv->format == FT_KV_E4M3, flags & FT_ROPE_ADJACENT, (cudaStream_t)stream));
+  return cu("ft_kv_append", ft::launch_kv_append(a, kv->format == FT_KV_E4M3, flags & FT_ROPE_ADJACENT, sms, (cudaStream_t)stream));
 }
 
 extern "C" ft_status ft_kv_attention(const ft_kv_cache* kv, const void* q, int64_t q_stride, float scale, void* out,

@@ -92,7 +92,7 @@ int64_t kv_evict_workspace(const ft_kv_cache& c);
 // The attention's split of `total` tiles over `sms` SMs: entries of a tile, tiles of a chunk, chunks used, chunks there are.
 void kv_geometry(const ft_kv_cache& c, int total, int sms, int64_t out[4]);
 
-cudaError_t launch_kv_append(const KvAppendArgs& a, bool e4m3, bool adjacent, cudaStream_t s);
+cudaError_t launch_kv_append(const KvAppendArgs& a, bool e4m3, bool adjacent, int sms, cudaStream_t s);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, bool e4m3, int device, int sms, cudaStream_t s);
 cudaError_t launch_kv_wait(int blocks, uint64_t limit_ns, int64_t arrive_ns, int32_t* lanes, cudaStream_t s);
 cudaError_t launch_kv_evict(const KvEvictArgs& a, int row_bytes, int device, int sms, cudaStream_t s);

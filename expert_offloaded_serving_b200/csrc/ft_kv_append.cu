@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;   // tokens of a group
+constexpr int kLone = 14;       // blocks of one token an SM has at most
 constexpr int kMaxHalf = 128;   // rot_dim / 2 at most
 
 struct Vec8 {
@@ -297,16 +298,17 @@ cudaError_t run(const KvAppendArgs& a, dim3 grid, int group, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_kv_append(const KvAppendArgs& a, bool e4m3, bool adjacent, cudaStream_t s) {
+cudaError_t launch_kv_append(const KvAppendArgs& a, bool e4m3, bool adjacent, int sms, cudaStream_t s) {
   // Few tokens: one a block, and several blocks a token while those leave SMs idle: the
-  // latency of one token's chain counts then.  Beyond two waves of blocks up to 4
-  // tokens share a block, whose 256 threads have their angles in one go.
-  const int64_t waves = 148 * 14;
-  const int group = (int)(a.T <= waves ? 1 : a.T >= waves * kMaxTokens ? kMaxTokens : a.T / waves);
+  // latency of one token's chain counts then.  Beyond kLone blocks an SM (a little over two waves) up to 4
+  // tokens share a block, whose 256 threads have their angles in one go: 8,191 tokens, 32 + 8 heads of
+  // 128, 37.8 us with 14 (7: 40.3, 28: 48.8), 3,000 tokens 20.4 (16.1 and 20.3), 16,384 tokens 71.5 (71.7 and 67.7).
+  const int64_t lone = (int64_t)sms * kLone;
+  const int group = (int)(a.T <= lone ? 1 : a.T >= lone * kMaxTokens ? kMaxTokens : a.T / lone);
   const int64_t groups = (a.T + group - 1) / group;
   const int64_t pieces = (int64_t)((a.q ? a.kv.Hq : 0) + 2 * a.kv.Hkv) * (a.kv.D >> 3);
   int share = 1;
-  while (share < 8 && a.T * share * 2 <= 148 && pieces > (int64_t)kThreads * share) share *= 2;
+  while (share < 8 && a.T * share * 2 <= sms && pieces > (int64_t)kThreads * share) share *= 2;
   const dim3 grid((unsigned)groups, (unsigned)share);
   if (e4m3) return adjacent ? run<true, true>(a, grid, group, s) : run<true, false>(a, grid, group, s);
   return adjacent ? run<false, true>(a, grid, group, s) : run<false, false>(a, grid, group, s);
