@@ -54,10 +54,15 @@ constexpr int kRows = 16;        // query heads of a group, which one warp takes
 // Tile and warps by what was measured: 32 entries halve the instructions around the
 // products, up to rows of 256 bytes (131,072 entries of 256 bytes 93 us, 16 entries a tile 96).
 // There 4 warps x 3 stages match 6 x 2 on long rows (93 and 92 us) and win on 64 sequences of 200
-// entries (12.4 against 15.3); rows of 128 bytes want 8 warps (a ragged batch 56.8 us, 59.7 with
-// 6; 16 x 8,000 entries and 64 heads over 4: 34.2, 36.1 with 12), rows of 96 too (16 heads over one: 29.6,
-// 33.1 with 12), rows of 64 want 16 (16 x 8,000 entries, 8 heads: 30.7, 33.4 with 8); beyond 256
+// entries (12.4 against 15.3); rows of 128 bytes want 8 warps (a ragged weighed batch of 48, 64 heads over 4
+// of 128 57.6 us, 60.9 with 6, 65.1 with 12; 16 x 8,000 entries of the same heads 34.9, 41.3 and 38.9), rows of 96 too (64 sequences
+// of 300 to 9,000 entries, 16 heads over one: 18.4, 21.2 with 12), rows of 64 want 16 (16 x 8,000
+// entries, 8 heads with a KV head each: 31.1, 35.2 with 8; with one for all 14.9 and 11.6); beyond 256
 // the registers of O leave room for 4.
+//
+// Registers: heads of 256 in E4M3 with more than 8 query heads a KV head hold 192 of O and q alone and spill
+// about 500 bytes a thread (12 sequences of 1,000 to 24,000 entries, 32 heads over 2: 49.5 us on a floor of 16); BF16 heads of
+// 256 and E4M3 heads of 192 and 64 with as many spill 24 to 130.
 constexpr int tile_of(int row_bytes) { return row_bytes <= 256 ? 32 : 16; }
 constexpr int warps_of(int row_bytes) { return row_bytes >= 256 ? 4 : row_bytes == 64 ? 16 : 8; }
 template <int RB>
@@ -858,8 +863,8 @@ struct JoinArgs {
 };
 
 // Warps of a block of k_kv_join: 32 an SM in all, as many blocks as the split has warps.  Measured
-// against half and double: 37 entries 6.6 us with 8 (4: 7.3, 16: 6.8), a weighed E4M3 batch 56.8
-// with 4 (2: 58.9, 8: 60.6).
+// against half and double: 37 entries 6.4 us with 8 (4: 6.8, 16: 6.4), a weighed E4M3 batch 57.6
+// with 4 (2: 65.0, 8: 61.3).
 constexpr int join_warps(int row_bytes) { return 32 / warps_of(row_bytes); }
 
 // What a sum with reference x counts for under the reference `both` >= x.
@@ -917,7 +922,7 @@ __device__ __forceinline__ void join_row(const JoinArgs& args, const Chunk& c) {
 }
 
 // A row in more parts than this has its lse found by the block together, not by each warp for itself:
-// 100,000 E4M3 entries and 16 heads of 128 34 us, 78 by warps alone; 11 ragged rows of up to 14,000
+// 100,000 E4M3 entries and 16 heads of 128 35 us, 78 by warps alone; 11 ragged rows of up to 14,000
 // entries, 48 heads over two of 256 48.4 (from 32 parts on 49.8, from 64 on 54.8).  Few parts cost less by warps (13 rows
 // of up to 171 entries 18.4 us so, 19.6 with the block's way in the kernel at all).
 constexpr int kManyParts = 16;

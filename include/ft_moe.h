@@ -591,7 +591,10 @@ typedef struct {
  * keeps none from one call for the next; calls that share one must be ordered
  * on the GPU, so two graphs that may run at the same time take two.  Reads
  * the shape, and whether mass and pos are there (room for FT_KV_MASS and
- * ft_kv_evict).  FT_ERR_INVALID on a bad shape. */
+ * ft_kv_evict).  With mass it grows with the whole pool, in use or not: 4
+ * bytes an entry and query head that shares it (their number rounded up to a power of
+ * two up to 16, above that to a multiple of 16), so 16 heads over E4M3 rows of
+ * 128 take a quarter of the cache again.  FT_ERR_INVALID on a bad shape. */
 FT_API ft_status ft_kv_workspace_bytes(const ft_kv_cache* kv, int64_t* bytes);
 
 /* How ft_kv_attention splits a batch of `tiles` tiles (below 2^30; a tile is
