@@ -533,8 +533,8 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
           top = fmaxf(top, fmaxf(fabsf(bf16_lo(q[ks][nb][i])), fabsf(bf16_hi(q[ks][nb][i]))));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent; 0 and 255: as it is
-      const bool usual = e > 14 && e < 255;
+      const int e = min((int)(__float_as_uint(top) >> 23), 254);  // biased exponent; next to an infinity the others have to fit all the same
+      const bool usual = e > 14;
       const float up = usual ? __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23) : 1.0f;
       const float down = usual ? __uint_as_float((uint32_t)(e - 14) << 23) : 1.0f;
 #pragma unroll

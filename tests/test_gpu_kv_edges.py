@@ -70,3 +70,21 @@ def test_one_entry_over_a_long_tail(gap, e4m3):
     want = 1.9921875 * (n - 1) / n
     assert (out[:, 1, :32].double() - want).abs().max() <= want * (2.0 ** -8 + sums)
     assert (lse[:, 1].double() - math.log(n)).abs().max() <= 2.0 ** -9
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_an_infinite_query_beside_a_large_one(e4m3):
+    """Every key is positive: an element of -inf makes every score -inf whatever the finite others are, one of +inf NaN."""
+    c = Cache([60], 8, 2, 64, 16, e4m3, seed=6)
+    at = c.place(0, torch.arange(60, device="cuda"))
+    c.k[at] = c.stored(torch.rand(60, 2, 64, device="cuda") + 0.5, c.k_scale)
+    q = queries(c, 1)
+    clean, _ = call(c, q, 0.125)
+    q[0, 1, 5], q[0, 1, 9] = -math.inf, 1e30
+    q[0, 2, 5], q[0, 2, 9] = math.inf, 1e30
+    q[0, 6, 5], q[0, 6, 9] = -math.inf, -3e38
+    out, lse = call(c, q, 0.125)
+    assert (out[0, [1, 6]] == 0).all() and (lse[0, [1, 6]] == -math.inf).all()
+    assert torch.isnan(out[0, 2]).all()
+    rest = [0, 3, 4, 5, 7]
+    assert torch.equal(out[0, rest], clean[0, rest])
