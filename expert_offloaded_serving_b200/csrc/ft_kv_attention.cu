@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(Ring<D * (E4M3 ? 1 : 2)>::kWarps * 32, 1) k_kv
   uint64_t* const full = s_full + warp * R::kStages;
   if (lane < R::kStages) tc::mbar_init(full + lane, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncwarp();  // lane 0 arrives at barriers that other lanes made
   if (tid == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&args.k_map) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&args.v_map) : "memory");
