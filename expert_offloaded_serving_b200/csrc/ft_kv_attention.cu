@@ -61,8 +61,8 @@ constexpr int kRows = 16;        // query heads of a group, which one warp takes
 // the registers of O leave room for 4.
 //
 // Registers: heads of 256 in E4M3 with more than 8 query heads a KV head hold 192 of O and q alone and spill
-// about 500 bytes a thread (12 sequences of 1,000 to 24,000 entries, 32 heads over 2: 49.5 us on a floor of 16); BF16 heads of
-// 256 and E4M3 heads of 192 and 64 with as many spill 24 to 130.
+// 676 bytes a thread (12 sequences of 1,000 to 24,000 entries, 32 heads over 2: 49.6 us on a floor of 16); BF16 heads of
+// 256 and E4M3 heads of 192 and 64 with as many spill 16 to 48.
 constexpr int tile_of(int row_bytes) { return row_bytes <= 256 ? 32 : 16; }
 constexpr int warps_of(int row_bytes) { return row_bytes >= 256 ? 4 : row_bytes == 64 ? 16 : 8; }
 template <int RB>
