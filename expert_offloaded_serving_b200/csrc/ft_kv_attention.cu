@@ -33,9 +33,10 @@
 // is known.
 //
 // Measured (one B200, a graph of passes): 1 x 131,071 entries, 64 query and 8 KV heads of 128, BF16
-// 91 us (5.9 TB/s; the slowest SMs end at 86, the mean one at 77: the share of the
+// 92 us (5.8 TB/s; the slowest SMs end at 86, the mean one at 77: the share of the
 // memory's rate that an SM gets differs by 13 %); 64 sequences of 300 to 16,000 entries
-// 163 us (6.1 TB/s, 6.2 in the split); 37 entries 6.5 us, two launches and four trips to memory.
+// 165 us (6.0 TB/s, 6.2 in the split); 48 of 500 to 12,000 in E4M3, 64 heads over 4 of 128, 57.6 us weighed
+// and 38.2 not; 37 entries 6.4 us, two launches and four trips to memory.
 #include "ft_gemm.h"
 #include "ft_kv.cuh"
 #include "ft_tc.cuh"
